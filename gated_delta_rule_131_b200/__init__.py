@@ -17,10 +17,19 @@ Entry points (same names as the C ABI):
 * :func:`recurrent_fwd` -- the token loop over whole sequences in either erase orientation
   (``gdn2_recurrent_fwd``);
 * :func:`block_prologue`, :func:`block_epilogue` -- the work around the mixer
-  in its block (``gdn2_block_prologue``, ``gdn2_block_epilogue``).
+  in its block (``gdn2_block_prologue``, ``gdn2_block_epilogue``);
+* :func:`block_prologue_bwd`, :func:`block_epilogue_bwd` -- gradients through
+  them (``gdn2_block_prologue_bwd``, ``gdn2_block_epilogue_bwd``);
+* :func:`layer_norm_fwd`, :func:`layer_norm_bwd` -- the norm in front of the
+  block's projections (``gdn2_layer_norm_fwd``, ``gdn2_layer_norm_bwd``);
+* :func:`act_pack`, :func:`act_unpack`, :class:`Act8` -- activations held in 8
+  bits between the forward and the backward pass (``gdn2_act_pack``,
+  ``gdn2_act_unpack``), which the backward calls read directly.
 """
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -78,6 +87,25 @@ def lib():
         L.gdn2_chunk_bwd_workspace_bytes.restype = ctypes.c_size_t
         L.gdn2_chunk_fwd_plan.argtypes = [ci] * 9 + [ctypes.POINTER(ChunkPlan)]
         L.gdn2_chunk_fwd_plan.restype = ci
+        cll = ctypes.c_longlong
+        L.gdn2_act_pack.argtypes = [vp] * 5 + [ci, ci, vp]
+        L.gdn2_act_pack.restype = ci
+        L.gdn2_act_unpack.argtypes = [vp] * 5 + [ci, ci, vp]
+        L.gdn2_act_unpack.restype = ci
+        L.gdn2_layer_norm_fwd.argtypes = [vp] * 4 + [ctypes.c_float] + [vp] * 6 + [cll, ci, ci, vp]
+        L.gdn2_layer_norm_fwd.restype = ci
+        L.gdn2_layer_norm_bwd.argtypes = [vp] * 10 + [cll, ci, ci, vp]
+        L.gdn2_layer_norm_bwd.restype = ci
+        L.gdn2_layer_norm_bwd_workspace_bytes.argtypes = [cll, ci]
+        L.gdn2_layer_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn2_block_epilogue_bwd.argtypes = [vp] * 9 + [cll, ci, ci, ci, vp]
+        L.gdn2_block_epilogue_bwd.restype = ci
+        L.gdn2_block_epilogue_bwd_workspace_bytes.argtypes = [cll, ci, ci]
+        L.gdn2_block_epilogue_bwd_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn2_block_prologue_bwd.argtypes = [vp] * 25 + [ci] * 6 + [vp, ci, vp]
+        L.gdn2_block_prologue_bwd.restype = ci
+        L.gdn2_block_prologue_bwd_workspace_bytes.argtypes = [ci] * 8
+        L.gdn2_block_prologue_bwd_workspace_bytes.restype = ctypes.c_size_t
         _lib = L
     return _lib
 
@@ -337,3 +365,286 @@ def decode_step(q, k, v, alpha, b, w, S, o=None, stream=None):
     if st != GDN2_OK:
         raise Gdn2Error(st, "gdn2_decode_step")
     return o
+
+
+# ------------------------------------------------------------------------------------------------
+# training operators of the block
+
+ACT_GROUP = 32          # channels that share a scale in an Act8
+ACT_MAX_TENSORS = 8     # GDN2_ACT_MAX_TENSORS in include/gdn2.h
+NORM_MAX_WIDTH = 8192   # GDN2_NORM_MAX_WIDTH in include/gdn2.h
+
+
+class Act8(NamedTuple):
+    """A tensor held in 8 bits: ``codes`` int8 in its shape, ``scales`` uint8 ``[..., ceil(D / 32)]``
+    for its last dimension ``D`` (the format is described in ``include/gdn2.h``)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+class LayerNormOut(NamedTuple):
+    """What :func:`layer_norm_fwd` returns; ``checkpoint`` is ``h`` as an :class:`Act8`, or None."""
+    y: torch.Tensor
+    h: torch.Tensor
+    mean: torch.Tensor
+    rstd: torch.Tensor
+    checkpoint: Optional[Act8]
+
+
+@contextlib.contextmanager
+def _launching(stream, *tensors):
+    """The device of ``tensors`` and the launch stream made current: outputs are allocated for that
+    stream, and inputs are kept until its work is done.  Yields the stream's handle."""
+    tensors = [t for t in tensors if t is not None]
+    _check_tensors(*tensors)
+    dev = tensors[0].device
+    with torch.cuda.device(dev):
+        own = torch.cuda.current_stream(dev)
+        if stream is None or stream == own:
+            yield _stream(own)
+            return
+        if stream.device != dev:
+            raise ValueError("gdn2: the stream is on another device than the tensors")
+        with torch.cuda.stream(stream):
+            yield _stream(stream)
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _shapes(what, expect, **tensors):
+    for name, t in tensors.items():
+        if t is not None and tuple(t.shape) != tuple(expect):
+            raise ValueError(f"gdn2: {what}: {name} has shape {tuple(t.shape)}, expected {tuple(expect)}")
+
+
+def _types(what, dtype, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"gdn2: {what}: {name} must be {dtype}")
+
+
+def _check_act8(what, name, a, shape):
+    _types(what, torch.int8, **{name + ".codes": a.codes})
+    _types(what, torch.uint8, **{name + ".scales": a.scales})
+    _shapes(what, shape, **{name + ".codes": a.codes})
+    _shapes(what, tuple(shape[:-1]) + (-(-shape[-1] // ACT_GROUP),), **{name + ".scales": a.scales})
+
+
+def _new_act8(shape, device):
+    return Act8(torch.empty(shape, dtype=torch.int8, device=device),
+                torch.empty(tuple(shape[:-1]) + (-(-shape[-1] // ACT_GROUP),), dtype=torch.uint8, device=device))
+
+
+def _rows(shape):
+    n = 1
+    for s in shape[:-1]:
+        n *= s
+    return n
+
+
+def _act_call(entry, first, second, third, shapes, dtype, stream):
+    n = len(shapes)
+    ptrs = [(ctypes.c_void_p * n)(*[t.data_ptr() for t in ts]) for ts in (first, second, third)]
+    rows = (ctypes.c_longlong * n)(*[_rows(s) for s in shapes])
+    width = (ctypes.c_int * n)(*[s[-1] for s in shapes])
+    st = getattr(lib(), entry)(*ptrs, rows, width, n, _DTYPES[dtype], stream)
+    if st != GDN2_OK:
+        raise Gdn2Error(st, entry)
+
+
+def act_pack(xs, stream=None):
+    """Hold a tensor, or a list of up to ``ACT_MAX_TENSORS`` of one dtype, in 8 bits: returns an
+    :class:`Act8` or a list of them.  See ``gdn2_act_pack`` in ``include/gdn2.h``."""
+    one = isinstance(xs, torch.Tensor)
+    xs = [xs] if one else list(xs)
+    if not xs:
+        return []
+    if xs[0].dtype not in _DTYPES or any(x.dtype != xs[0].dtype for x in xs):
+        raise ValueError("gdn2: act_pack: the tensors must share dtype float32 or bfloat16")
+    if any(x.dim() < 1 or x.shape[-1] < 1 for x in xs):
+        raise ValueError("gdn2: act_pack: a tensor needs a last dimension of at least 1")
+    with _launching(stream, *xs) as s:
+        out = [_new_act8(x.shape, x.device) for x in xs]
+        _act_call("gdn2_act_pack", xs, [a.codes for a in out], [a.scales for a in out], [x.shape for x in xs],
+                  xs[0].dtype, s)
+    return out[0] if one else out
+
+
+def act_unpack(acts, dtype=torch.bfloat16, stream=None):
+    """The values that an :class:`Act8`, or a list of them, holds (exact in either dtype)."""
+    one = isinstance(acts, Act8)
+    acts = [acts] if one else list(acts)
+    if not acts:
+        return []
+    if dtype not in _DTYPES:
+        raise ValueError("gdn2: act_unpack: dtype must be float32 or bfloat16")
+    for a in acts:
+        if a.codes.dim() < 1 or a.codes.shape[-1] < 1:
+            raise ValueError("gdn2: act_unpack: a tensor needs a last dimension of at least 1")
+        _check_act8("act_unpack", "act", a, a.codes.shape)
+    with _launching(stream, *[t for a in acts for t in a]) as s:
+        out = [torch.empty(a.codes.shape, dtype=dtype, device=a.codes.device) for a in acts]
+        _act_call("gdn2_act_unpack", [a.codes for a in acts], [a.scales for a in acts], out, [x.shape for x in out],
+                  dtype, s)
+    return out[0] if one else out
+
+
+def layer_norm_fwd(x, weight, bias=None, residual=None, eps=1e-5, checkpoint=False, stats=True, stream=None):
+    """Layer norm over the last dimension, of ``h = x + residual``: returns a :class:`LayerNormOut`.
+
+    ``h`` is ``x`` itself without a residual; ``mean`` and ``rstd`` (float32, one per row) are None
+    with ``stats=False``; ``checkpoint=True`` also returns ``h`` held in 8 bits.  See
+    ``gdn2_layer_norm_fwd`` in ``include/gdn2.h``.
+    """
+    if x.dtype not in _DTYPES:
+        raise ValueError("gdn2: layer_norm_fwd: x must be float32 or bfloat16")
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("gdn2: layer_norm_fwd: x needs a last dimension of at least 1")
+    D = x.shape[-1]
+    _types("layer_norm_fwd", x.dtype, residual=residual)
+    _types("layer_norm_fwd", torch.float32, weight=weight, bias=bias)
+    _shapes("layer_norm_fwd", x.shape, residual=residual)
+    _shapes("layer_norm_fwd", (D,), weight=weight, bias=bias)
+    with _launching(stream, x, weight, bias, residual) as s:
+        y = torch.empty_like(x)
+        h = None if residual is None else torch.empty_like(x)
+        mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if stats else None
+                      for _ in range(2))
+        ck = _new_act8(x.shape, x.device) if checkpoint else None
+        st = lib().gdn2_layer_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(h),
+                                       _ptr(mean), _ptr(rstd), *([_ptr(t) for t in ck] if ck else (None, None)),
+                                       _rows(x.shape), D, _DTYPES[x.dtype], s)
+        if st != GDN2_OK:
+            raise Gdn2Error(st, "gdn2_layer_norm_fwd")
+    return LayerNormOut(y, x if h is None else h, mean, rstd, ck)
+
+
+def layer_norm_bwd(dy, h, mean, rstd, weight, dh=None, want_dbias=True, stream=None):
+    """Gradients through :func:`layer_norm_fwd`: ``(dx, dweight, dbias)``, ``dx`` being the gradient of
+    ``x`` and of ``residual``, with ``dh`` (the gradient that reaches ``h`` past the norm) added.
+
+    ``h`` is the forward's ``h`` or its :class:`Act8` checkpoint.  ``dbias`` is None unless
+    ``want_dbias``.  See ``gdn2_layer_norm_bwd`` in ``include/gdn2.h``.
+    """
+    if dy.dtype not in _DTYPES:
+        raise ValueError("gdn2: layer_norm_bwd: dy must be float32 or bfloat16")
+    if dy.dim() < 1 or dy.shape[-1] < 1:
+        raise ValueError("gdn2: layer_norm_bwd: dy needs a last dimension of at least 1")
+    D = dy.shape[-1]
+    _types("layer_norm_bwd", dy.dtype, dh=dh)
+    _types("layer_norm_bwd", torch.float32, mean=mean, rstd=rstd, weight=weight)
+    _shapes("layer_norm_bwd", dy.shape, dh=dh)
+    _shapes("layer_norm_bwd", dy.shape[:-1], mean=mean, rstd=rstd)
+    _shapes("layer_norm_bwd", (D,), weight=weight)
+    codes, scales = _saved("layer_norm_bwd", "h", h, dy)
+    with _launching(stream, dy, codes, scales, mean, rstd, weight, dh) as s:
+        dx = torch.empty_like(dy)
+        dweight = torch.empty(D, dtype=torch.float32, device=dy.device)
+        dbias = torch.empty_like(dweight) if want_dbias else None
+        st = lib().gdn2_layer_norm_bwd(_ptr(dy), _ptr(codes), _ptr(scales), _ptr(mean), _ptr(rstd), _ptr(weight),
+                                       _ptr(dh), _ptr(dx), _ptr(dweight), _ptr(dbias), _rows(dy.shape), D,
+                                       _DTYPES[dy.dtype], s)
+        if st != GDN2_OK:
+            raise Gdn2Error(st, "gdn2_layer_norm_bwd")
+    return dx, dweight, dbias
+
+
+def _saved(what, name, x, like):
+    """A saved activation as (values or codes, scales or None), checked against its gradient."""
+    if isinstance(x, Act8):
+        _check_act8(what, name, x, like.shape)
+        return x.codes, x.scales
+    _types(what, like.dtype, **{name: x})
+    _shapes(what, like.shape, **{name: x})
+    return x, None
+
+
+def layer_norm_bwd_workspace_bytes(tokens, width) -> int:
+    """Device bytes ``layer_norm_bwd`` takes from the library's pool for this shape."""
+    return int(lib().gdn2_layer_norm_bwd_workspace_bytes(tokens, width))
+
+
+def block_epilogue_bwd(o, gate, norm_weight, dy, stream=None):
+    """Gradients through :func:`block_epilogue`: ``(do, dgate, dnorm_weight)``.
+
+    ``o`` and ``gate`` are the forward's inputs, or both :class:`Act8` checkpoints of them.  See
+    ``gdn2_block_epilogue_bwd`` in ``include/gdn2.h``.
+    """
+    if dy.dtype not in _DTYPES:
+        raise ValueError("gdn2: block_epilogue_bwd: dy must be float32 or bfloat16")
+    if dy.dim() < 2:
+        raise ValueError("gdn2: block_epilogue_bwd: dy must be [..., H, d_v]")
+    if isinstance(o, Act8) != isinstance(gate, Act8):
+        raise ValueError("gdn2: block_epilogue_bwd: o and gate are both tensors or both Act8")
+    H, dv = dy.shape[-2], dy.shape[-1]
+    _types("block_epilogue_bwd", torch.float32, norm_weight=norm_weight)
+    _shapes("block_epilogue_bwd", (dv,), norm_weight=norm_weight)
+    oc, osc = _saved("block_epilogue_bwd", "o", o, dy)
+    gc, gsc = _saved("block_epilogue_bwd", "gate", gate, dy)
+    with _launching(stream, oc, osc, gc, gsc, norm_weight, dy) as s:
+        do, dgate = torch.empty_like(dy), torch.empty_like(dy)
+        dnorm_weight = torch.empty(dv, dtype=torch.float32, device=dy.device)
+        st = lib().gdn2_block_epilogue_bwd(_ptr(oc), _ptr(gc), _ptr(osc), _ptr(gsc), _ptr(norm_weight), _ptr(dy),
+                                           _ptr(do), _ptr(dgate), _ptr(dnorm_weight), _rows(dy.shape[:-1]), H, dv,
+                                           _DTYPES[dy.dtype], s)
+        if st != GDN2_OK:
+            raise Gdn2Error(st, "gdn2_block_epilogue_bwd")
+    return do, dgate, dnorm_weight
+
+
+def block_epilogue_bwd_workspace_bytes(tokens, H, d_v) -> int:
+    """Device bytes ``block_epilogue_bwd`` takes from the library's pool for this shape."""
+    return int(lib().gdn2_block_epilogue_bwd_workspace_bytes(tokens, H, d_v))
+
+
+def block_prologue_bwd(xq, xk, xv, xa, xb, xw, conv_q, conv_k, conv_v, dq, dk, dv, dalpha, db, dw, cu_seqlens=None,
+                       stream=None):
+    """Gradients through :func:`block_prologue` from those that :func:`chunk_bwd` returns:
+    ``(dxq, dxk, dxv, dxa, dxb, dxw, dconv_q, dconv_k, dconv_v)``.
+
+    The six inputs are the forward's, or all :class:`Act8` checkpoints of them.  In a packed batch,
+    rows behind the last sequence keep whatever memory their gradients were given.  See
+    ``gdn2_block_prologue_bwd`` in ``include/gdn2.h``.
+    """
+    what = "block_prologue_bwd"
+    xs, grads, convs = (xq, xk, xv, xa, xb, xw), (dq, dk, dv, dalpha, db, dw), (conv_q, conv_k, conv_v)
+    if dq.dtype not in _DTYPES or any(g.dtype != dq.dtype for g in grads):
+        raise ValueError("gdn2: block_prologue_bwd: the gradients must share dtype float32 or bfloat16")
+    packed8 = isinstance(xq, Act8)
+    if any(isinstance(x, Act8) != packed8 for x in xs):
+        raise ValueError("gdn2: block_prologue_bwd: the saved inputs are all tensors or all Act8")
+    if dq.dim() != (4 if cu_seqlens is None else 3):
+        raise ValueError("gdn2: block_prologue_bwd: gradients are [B, T, H, d], or [T, H, d] with cu_seqlens")
+    if cu_seqlens is None:
+        B, T, H, d_k = dq.shape
+    else:
+        _types(what, torch.int32, cu_seqlens=cu_seqlens)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("gdn2: block_prologue_bwd: cu_seqlens must be [B + 1]")
+        B = cu_seqlens.numel() - 1
+        T, H, d_k = dq.shape
+    d_v = dv.shape[-1]
+    K = conv_q.shape[-1]
+    _shapes(what, dq.shape, dk=dk, dalpha=dalpha, db=db)
+    _shapes(what, tuple(dq.shape[:-1]) + (d_v,), dv=dv, dw=dw)
+    _types(what, torch.float32, conv_q=conv_q, conv_k=conv_k, conv_v=conv_v)
+    _shapes(what, (H * d_k, K), conv_q=conv_q, conv_k=conv_k)
+    _shapes(what, (H * d_v, K), conv_v=conv_v)
+    saved = [_saved(what, n, x, g) for n, x, g in zip(("xq", "xk", "xv", "xa", "xb", "xw"), xs, grads)]
+    with _launching(stream, *grads, *[t for pair in saved for t in pair], *convs, cu_seqlens) as s:
+        dxs = [torch.empty_like(g) for g in grads]
+        dconv = [torch.empty_like(c) for c in convs]
+        scales = (ctypes.c_void_p * 6)(*[sc.data_ptr() for _, sc in saved]) if packed8 else None
+        st = lib().gdn2_block_prologue_bwd(*[_ptr(c) for c, _ in saved], scales, *[_ptr(c) for c in convs],
+                                           *[_ptr(g) for g in grads], *[_ptr(t) for t in dxs],
+                                           *[_ptr(t) for t in dconv], B, T, H, d_k, d_v, K, _ptr(cu_seqlens),
+                                           _DTYPES[dq.dtype], s)
+        if st != GDN2_OK:
+            raise Gdn2Error(st, "gdn2_block_prologue_bwd")
+    return (*dxs, *dconv)
+
+
+def block_prologue_bwd_workspace_bytes(B, T, H, d_k, d_v, conv_len, packed=False, dtype=torch.bfloat16) -> int:
+    """Device bytes ``block_prologue_bwd`` takes from the library's pool for this shape."""
+    return int(lib().gdn2_block_prologue_bwd_workspace_bytes(B, T, H, d_k, d_v, conv_len, int(bool(packed)),
+                                                             _DTYPES[dtype]))

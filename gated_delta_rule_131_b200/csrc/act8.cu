@@ -1,0 +1,223 @@
+// Activation checkpoints in 8 bits (format: act8.cuh): packing, unpacking, and the column sums that
+// finish the weight gradients of the training operators.
+//
+// Packing and unpacking are HBM-bound streams: each value is read once and written once.
+#include <algorithm>
+
+#include "act8.cuh"
+
+namespace gdn2 {
+namespace {
+
+constexpr int NU = 4;  // vectors that a lane has in flight
+
+// Rows whose width is a multiple of 32: groups lie end to end over the whole tensor, so a lane's
+// vector index needs no row.  One tensor per grid row.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) act_pack_flat_kernel(const ActArgs a) {
+  const ActTensor t = a.t[blockIdx.y];
+  const long long nvec = t.rows * t.width / VEC;  // a multiple of the lanes of a group
+  const LaneVec<T, VEC> *x = static_cast<const LaneVec<T, VEC> *>(t.x);
+  LaneVec<int8_t, VEC> *c = reinterpret_cast<LaneVec<int8_t, VEC> *>(t.codes);
+  for (long long b = (long long)blockIdx.x * (256 * NU); b < nvec; b += (long long)gridDim.x * (256 * NU)) {
+    LaneVec<T, VEC> r[NU];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const long long i = b + u * 256 + threadIdx.x;
+      if (i < nvec) r[u] = x[i];
+    }
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const long long i = b + u * 256 + threadIdx.x;
+      float f[VEC];
+      widen(r[u], f);
+      if (i >= nvec)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) f[k] = 0.f;
+      uint32_t s;
+      const LaneVec<int8_t, VEC> v = act8_encode<VEC>(f, s);
+      if (i < nvec) {
+        c[i] = v;
+        if (i % (ACT_GROUP / VEC) == 0) t.scales[i / (ACT_GROUP / VEC)] = (uint8_t)s;
+      }
+    }
+  }
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) act_unpack_flat_kernel(const ActArgs a) {
+  const ActTensor t = a.t[blockIdx.y];
+  const long long nvec = t.rows * t.width / VEC;
+  const LaneVec<int8_t, VEC> *c = reinterpret_cast<const LaneVec<int8_t, VEC> *>(t.codes);
+  LaneVec<T, VEC> *x = static_cast<LaneVec<T, VEC> *>(t.x);
+  for (long long b = (long long)blockIdx.x * (256 * NU); b < nvec; b += (long long)gridDim.x * (256 * NU)) {
+    LaneVec<int8_t, VEC> r[NU];
+    uint32_t s[NU];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const long long i = b + u * 256 + threadIdx.x;
+      if (i < nvec) {
+        r[u] = c[i];
+        s[u] = t.scales[i / (ACT_GROUP / VEC)];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const long long i = b + u * 256 + threadIdx.x;
+      if (i < nvec) {
+        float f[VEC];
+        widen(r[u], act8_unit(s[u]), f);
+        LaneVec<T, VEC> v;
+        narrow(f, v);
+        x[i] = v;
+      }
+    }
+  }
+}
+
+// Rows that end inside a group: a warp takes 32 * VEC * NU channels of one row at a time.
+template <typename T, int VEC, bool PACK>
+__global__ void __launch_bounds__(256) act_rows_kernel(const ActArgs a) {
+  constexpr int SPAN = 32 * VEC * NU;
+  const ActTensor t = a.t[blockIdx.y];
+  const int per_row = (t.width + SPAN - 1) / SPAN, lane = threadIdx.x & 31;
+  const int groups = (t.width + ACT_GROUP - 1) / ACT_GROUP;
+  const long long tasks = t.rows * per_row, step = (long long)gridDim.x * 8;
+  for (long long k = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); k < tasks; k += step) {
+    const long long row = k / per_row;
+    const int c0 = (int)(k - row * per_row) * SPAN + lane * VEC;
+    T *x = static_cast<T *>(t.x) + (size_t)row * t.width;
+    int8_t *codes = t.codes + (size_t)row * t.width;
+    uint8_t *scales = t.scales + (size_t)row * groups;
+    LaneVec<T, VEC> r[NU];
+    LaneVec<int8_t, VEC> q[NU];
+    uint32_t s[NU];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int c = c0 + u * 32 * VEC;  // VEC divides the width: a vector is inside the row or outside
+      if (c < t.width) {
+        if constexpr (PACK) {
+          r[u] = *reinterpret_cast<const LaneVec<T, VEC> *>(x + c);
+        } else {
+          q[u] = *reinterpret_cast<const LaneVec<int8_t, VEC> *>(codes + c);
+          s[u] = scales[c / ACT_GROUP];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int c = c0 + u * 32 * VEC;
+      float f[VEC];
+      if constexpr (PACK) {
+        widen(r[u], f);
+        if (c >= t.width)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) f[i] = 0.f;
+        uint32_t sc;
+        const LaneVec<int8_t, VEC> v = act8_encode<VEC>(f, sc);
+        if (c < t.width) {
+          *reinterpret_cast<LaneVec<int8_t, VEC> *>(codes + c) = v;
+          if (c % ACT_GROUP == 0) scales[c / ACT_GROUP] = (uint8_t)sc;
+        }
+      } else if (c < t.width) {
+        widen(q[u], act8_unit(s[u]), f);
+        LaneVec<T, VEC> v;
+        narrow(f, v);
+        *reinterpret_cast<LaneVec<T, VEC> *>(x + c) = v;
+      }
+    }
+  }
+}
+
+// Which kernel serves the call: one launch handles tensors of one kind.  16-byte vectors where every
+// row starts on one (width * element size a multiple of 16), single values elsewhere.
+template <typename T, bool PACK>
+cudaError_t act_t(const ActArgs &all, cudaStream_t stream) {
+  constexpr int V = 16 / sizeof(T);
+  for (int kind = 0; kind < 3; ++kind) {  // 0: whole groups, 1: aligned rows, 2: any width
+    ActArgs a{};
+    long long most = 0;
+    for (int i = 0; i < all.count; ++i) {
+      const ActTensor &t = all.t[i];
+      const int k = t.width % ACT_GROUP == 0 ? 0 : t.width % V == 0 ? 1 : 2;
+      if (k != kind || t.rows == 0) continue;
+      a.t[a.count++] = t;
+      const long long span = 32 * NU * (kind == 2 ? 1 : V);
+      most = std::max(most, kind == 0 ? (t.rows * t.width + 8 * span - 1) / (8 * span)
+                                      : (t.rows * ((t.width + span - 1) / span) + 7) / 8);
+    }
+    if (a.count == 0) continue;
+    const dim3 grid((unsigned)std::min<long long>(most, 1 << 20), a.count);
+    note_launch();
+    if (kind == 0) {
+      if (PACK) act_pack_flat_kernel<T, V><<<grid, 256, 0, stream>>>(a);
+      else act_unpack_flat_kernel<T, V><<<grid, 256, 0, stream>>>(a);
+    } else if (kind == 1) {
+      act_rows_kernel<T, V, PACK><<<grid, 256, 0, stream>>>(a);
+    } else {
+      act_rows_kernel<T, 1, PACK><<<grid, 256, 0, stream>>>(a);
+    }
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+// A block sums 32 columns: warp w takes the rows w, w + 8, ... (lane = column), then the eight warps'
+// sums are added in order.
+__global__ void __launch_bounds__(256) colsum_kernel(const ColSumArgs a) {
+  __shared__ float part[8][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (col < a.ncols) {
+    const float *p = a.parts + col;
+#pragma unroll 8
+    for (int r = warp; r < a.nparts; r += 8) s += p[(size_t)r * a.ncols];
+  }
+  part[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && col < a.ncols) {
+#pragma unroll
+    for (int w = 1; w < 8; ++w) s += part[w][lane];
+    const int k = col < a.end[0] ? 0 : col < a.end[1] ? 1 : 2;
+    if (a.out[k]) a.out[k][col - (k ? a.end[k - 1] : 0)] = s;
+  }
+}
+
+}  // namespace
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      sms <= 0) {
+    cudaGetLastError();  // no device: the sizes below are host arithmetic only
+    sms = 148;
+  }
+  return sms;
+}
+
+cudaError_t launch_colsum(const ColSumArgs &a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)((a.ncols + 31) / 32));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, colsum_kernel, a);
+}
+
+cudaError_t launch_act_pack(const ActArgs &a, bool bf16, cudaStream_t stream) {
+  return bf16 ? act_t<__nv_bfloat16, true>(a, stream) : act_t<float, true>(a, stream);
+}
+
+cudaError_t launch_act_unpack(const ActArgs &a, bool bf16, cudaStream_t stream) {
+  return bf16 ? act_t<__nv_bfloat16, false>(a, stream) : act_t<float, false>(a, stream);
+}
+
+}  // namespace gdn2

@@ -78,6 +78,67 @@ struct BlockEpilogueArgs {
   int H, dv;
 };
 
+// Tensors of one gdn2_act_pack / gdn2_act_unpack call (validated by the API layer).
+constexpr int ACT_TENSORS = 8;
+struct ActTensor {
+  void *x;          // values [rows, width]
+  int8_t *codes;    // [rows, width]
+  uint8_t *scales;  // [rows, ceil(width / 32)]
+  long long rows;
+  int width;
+};
+struct ActArgs {
+  ActTensor t[ACT_TENSORS];
+  int count;
+};
+
+// Arguments of the layer norm and its backward (validated by the API layer); widths up to LN_MAX_WIDTH.
+constexpr int LN_MAX_WIDTH = 8192;
+struct NormFwdArgs {
+  const void *x, *residual;   // [rows, width]; residual or nullptr
+  const float *weight, *bias; // [width]; bias or nullptr
+  float eps;
+  void *y, *h;                // [rows, width]; h (x + residual, rounded) with a residual only
+  float *mean, *rstd;         // [rows] or nullptr
+  int8_t *codes;              // h in 8 bits, or nullptr
+  uint8_t *scales;
+  long long rows;
+  int width;
+};
+struct NormBwdArgs {
+  const void *dy, *h;         // h in dtype, or its codes where scales is set
+  const uint8_t *scales;
+  const float *mean, *rstd, *weight;
+  const void *dh;             // gradient that reaches h past the norm, or nullptr
+  void *dx;
+  float *dweight, *dbias;     // dbias or nullptr
+  long long rows;
+  int width;
+};
+
+// Arguments of the backward of the block epilogue / prologue (validated by the API layer).  Saved
+// activations are in dtype, or in 8 bits where their scales are set.
+struct EpilogueBwdArgs {
+  const void *o, *z, *dy;              // [tokens, H, d_v]
+  const uint8_t *o_scales, *z_scales;
+  const float *g;                      // [d_v]
+  void *dout, *dz;
+  float *dg;                           // [d_v]
+  long long rows;                      // tokens * H
+  int dv;
+};
+struct PrologueBwdArgs {
+  const void *x[6];             // x_q, x_k, x_v, x_alpha, x_b, x_w: [tokens, H, d]
+  const uint8_t *scales[6];     // all null, or all set
+  const float *W[3];            // taps of q, k, v: [H * d, K]
+  const void *d[6];             // gradients of q, k, v, alpha, b, w
+  void *dx[6];
+  float *dW[3];
+  const int32_t *cu;
+  int B, T, H, dk, dv, K;
+  long long tokens;
+};
+
 // Arguments of one gdn2_chunk_bwd call (validated by the API layer).
 struct BwdArgs {
   const void *q, *k, *v, *alpha, *b, *w, *dO;  // forward inputs and dL/do, [tokens, H, d]
@@ -90,6 +151,8 @@ struct BwdArgs {
 
 // Host side: every kernel launch of the library is counted here.
 void note_launch();
+// SMs of the current device (148, a B200's, if there is none).
+int sm_count();
 
 // Launchers (return the CUDA error of the launch).
 cudaError_t launch_chunk_simt(const ChunkArgs &a, bool bf16, cudaStream_t stream);
@@ -122,5 +185,16 @@ cudaError_t launch_decode(const DecodeArgs &a, bool bf16, cudaStream_t stream);
 cudaError_t launch_recurrent(const RecurrentArgs &a, bool bf16, bool r2, cudaStream_t stream);
 cudaError_t launch_block_prologue(const BlockPrologueArgs &p, bool bf16, cudaStream_t stream);
 cudaError_t launch_block_epilogue(const BlockEpilogueArgs &p, bool bf16, cudaStream_t stream);
+// The training operators of the block.  The backward passes write rows of partial weight gradients
+// into a workspace of the given bytes (for the current device) and sum them in a second launch.
+cudaError_t launch_act_pack(const ActArgs &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_act_unpack(const ActArgs &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_norm_fwd(const NormFwdArgs &a, bool bf16, cudaStream_t stream);
+size_t norm_bwd_workspace_bytes(long long rows, int width);
+cudaError_t launch_norm_bwd(const NormBwdArgs &a, bool bf16, void *ws, cudaStream_t stream);
+size_t epilogue_bwd_workspace_bytes(long long rows, int dv);
+cudaError_t launch_epilogue_bwd(const EpilogueBwdArgs &a, bool bf16, void *ws, cudaStream_t stream);
+size_t prologue_bwd_workspace_bytes(long long tokens, int H, int dk, int dv, int K, bool bf16);
+cudaError_t launch_prologue_bwd(const PrologueBwdArgs &a, bool bf16, void *ws, cudaStream_t stream);
 
 }  // namespace gdn2

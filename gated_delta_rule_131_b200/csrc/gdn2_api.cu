@@ -1,6 +1,7 @@
 // C ABI of the gdn2 library: argument validation, dispatch, status strings.
 // See include/gdn2.h for the contract of every entry point.
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <mutex>
 
@@ -86,6 +87,25 @@ cudaError_t run_chunk_bwd(const gdn2::BwdArgs &a, bool bf16, cudaStream_t stream
   if ((err = workspace_pool(&pool)) != cudaSuccess) return err;
   if ((err = cudaMallocFromPoolAsync(&ws, bytes, pool, stream)) != cudaSuccess) return err;
   err = gdn2::launch_chunk_bwd(a, bf16, ws, stream);
+  const cudaError_t ferr = cudaFreeAsync(ws, stream);
+  return err == cudaSuccess ? ferr : err;
+}
+
+// A launcher over `bytes` of workspace from the pool, returned to it on `stream`.  Inside a stream
+// capture the workspace belongs to the captured graph; the pool itself may be created there too,
+// which needs the relaxed capture mode for this thread.
+template <typename F>
+cudaError_t with_workspace(size_t bytes, cudaStream_t stream, F launch) {
+  cudaMemPool_t pool;
+  void *ws = nullptr;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaError_t err = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (err != cudaSuccess) return err;
+  err = workspace_pool(&pool);
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (err != cudaSuccess) return err;
+  if ((err = cudaMallocFromPoolAsync(&ws, bytes, pool, stream)) != cudaSuccess) return err;
+  err = launch(ws);
   const cudaError_t ferr = cudaFreeAsync(ws, stream);
   return err == cudaSuccess ? ferr : err;
 }
@@ -338,6 +358,185 @@ gdn2_status gdn2_decode_step(const void *q, const void *k, const void *v, const 
   gdn2::DecodeArgs a{q, k, v, alpha, b, w, S, o, B, H, d_k, d_v};
   const cudaError_t err = gdn2::launch_decode(a, dtype == GDN2_BF16, (cudaStream_t)stream);
   return err == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+gdn2_status finish(cudaError_t err) { return err == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA; }
+
+// Validation shared by gdn2_act_pack and gdn2_act_unpack.
+gdn2_status check_act(void *const *x, int8_t *const *codes, uint8_t *const *scales, const long long *rows,
+                      const int *width, int count, gdn2_dtype dtype, gdn2::ActArgs *a) {
+  if (count < 0) return GDN2_ERR_INVALID_ARG;
+  if (dtype != GDN2_F32 && dtype != GDN2_BF16) return GDN2_ERR_INVALID_ARG;
+  if (count > GDN2_ACT_MAX_TENSORS) return GDN2_ERR_UNSUPPORTED;
+  if (count > 0 && (!x || !codes || !scales || !rows || !width)) return GDN2_ERR_INVALID_ARG;
+  *a = gdn2::ActArgs{};
+  for (int i = 0; i < count; ++i) {
+    if (rows[i] < 0 || width[i] <= 0 || !fits(rows[i], (long long)width[i] + 31, 4, 1)) return GDN2_ERR_INVALID_ARG;
+    if (rows[i] == 0) continue;
+    for (const void *p : {(const void *)x[i], (const void *)codes[i], (const void *)scales[i]})
+      if (!p || !aligned16(p)) return GDN2_ERR_INVALID_ARG;
+    a->t[a->count++] = gdn2::ActTensor{x[i], codes[i], scales[i], rows[i], width[i]};
+  }
+  return GDN2_OK;
+}
+
+// Sizes of the layer norm: rows, and a width that the registers of one block hold.
+gdn2_status check_norm(long long tokens, int width, gdn2_dtype dtype) {
+  if (tokens < 0 || width <= 0) return GDN2_ERR_INVALID_ARG;
+  if (dtype != GDN2_F32 && dtype != GDN2_BF16) return GDN2_ERR_INVALID_ARG;
+  if (width > gdn2::LN_MAX_WIDTH) return GDN2_ERR_UNSUPPORTED;
+  return fits(tokens, (long long)width + 31, 4, 1) ? GDN2_OK : GDN2_ERR_INVALID_ARG;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn2_status gdn2_act_pack(const void *const *x, int8_t *const *codes, uint8_t *const *scales, const long long *rows,
+                          const int *width, int count, gdn2_dtype dtype, gdn2_stream_t stream) {
+  gdn2::ActArgs a;
+  const gdn2_status st = check_act(const_cast<void *const *>(x), codes, scales, rows, width, count, dtype, &a);
+  if (st != GDN2_OK || a.count == 0) return st;
+  return finish(gdn2::launch_act_pack(a, dtype == GDN2_BF16, (cudaStream_t)stream));
+}
+
+gdn2_status gdn2_act_unpack(const int8_t *const *codes, const uint8_t *const *scales, void *const *x,
+                            const long long *rows, const int *width, int count, gdn2_dtype dtype,
+                            gdn2_stream_t stream) {
+  gdn2::ActArgs a;
+  const gdn2_status st = check_act(x, const_cast<int8_t *const *>(codes), const_cast<uint8_t *const *>(scales), rows,
+                                   width, count, dtype, &a);
+  if (st != GDN2_OK || a.count == 0) return st;
+  return finish(gdn2::launch_act_unpack(a, dtype == GDN2_BF16, (cudaStream_t)stream));
+}
+
+gdn2_status gdn2_layer_norm_fwd(const void *x, const void *residual, const float *weight, const float *bias, float eps,
+                                void *y, void *h, float *mean, float *rstd, int8_t *h_codes, uint8_t *h_scales,
+                                long long tokens, int width, gdn2_dtype dtype, gdn2_stream_t stream) {
+  const gdn2_status st = check_norm(tokens, width, dtype);
+  if (st != GDN2_OK) return st;
+  if (!(eps >= 0.f) || eps > FLT_MAX) return GDN2_ERR_INVALID_ARG;  // NaN and infinity too
+  if ((residual != nullptr) != (h != nullptr) || (mean != nullptr) != (rstd != nullptr) ||
+      (h_codes != nullptr) != (h_scales != nullptr))
+    return GDN2_ERR_INVALID_ARG;
+  if (!weight || !aligned16(weight) || !aligned16(bias)) return GDN2_ERR_INVALID_ARG;
+  if (!aligned4(mean) || !aligned4(rstd)) return GDN2_ERR_INVALID_ARG;
+  if (tokens == 0) return GDN2_OK;
+  if (!x || !y) return GDN2_ERR_INVALID_ARG;
+  for (const void *p : {x, residual, (const void *)y, (const void *)h, (const void *)h_codes, (const void *)h_scales})
+    if (!aligned16(p)) return GDN2_ERR_INVALID_ARG;
+  const gdn2::NormFwdArgs a{x, residual, weight, bias, eps, y, h, mean, rstd, h_codes, h_scales, tokens, width};
+  return finish(gdn2::launch_norm_fwd(a, dtype == GDN2_BF16, (cudaStream_t)stream));
+}
+
+gdn2_status gdn2_layer_norm_bwd(const void *dy, const void *h, const uint8_t *h_scales, const float *mean,
+                                const float *rstd, const float *weight, const void *dh, void *dx, float *dweight,
+                                float *dbias, long long tokens, int width, gdn2_dtype dtype, gdn2_stream_t stream) {
+  const gdn2_status st = check_norm(tokens, width, dtype);
+  if (st != GDN2_OK) return st;
+  if (!weight || !aligned16(weight) || !dweight || !aligned4(dweight) || !aligned4(dbias)) return GDN2_ERR_INVALID_ARG;
+  if (tokens > 0) {
+    for (const void *p : {dy, h, (const void *)dx})
+      if (!p || !aligned16(p)) return GDN2_ERR_INVALID_ARG;
+    if (!aligned16(h_scales) || !aligned16(dh)) return GDN2_ERR_INVALID_ARG;
+    if (!mean || !rstd || !aligned4(mean) || !aligned4(rstd)) return GDN2_ERR_INVALID_ARG;
+  }
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (tokens == 0) {  // sums over no rows
+    cudaError_t err = cudaMemsetAsync(dweight, 0, width * sizeof(float), s);
+    if (err == cudaSuccess && dbias) err = cudaMemsetAsync(dbias, 0, width * sizeof(float), s);
+    return finish(err);
+  }
+  const gdn2::NormBwdArgs a{dy, h, h_scales, mean, rstd, weight, dh, dx, dweight, dbias, tokens, width};
+  return finish(with_workspace(gdn2::norm_bwd_workspace_bytes(tokens, width), s,
+                               [&](void *ws) { return gdn2::launch_norm_bwd(a, dtype == GDN2_BF16, ws, s); }));
+}
+
+size_t gdn2_layer_norm_bwd_workspace_bytes(long long tokens, int width) {
+  if (tokens <= 0 || width <= 0 || width > gdn2::LN_MAX_WIDTH) return 0;
+  return gdn2::norm_bwd_workspace_bytes(tokens, width);
+}
+
+gdn2_status gdn2_block_epilogue_bwd(const void *o, const void *gate, const uint8_t *o_scales,
+                                    const uint8_t *gate_scales, const float *norm_weight, const void *dy, void *d_o,
+                                    void *dgate, float *dnorm_weight, long long tokens, int H, int d_v,
+                                    gdn2_dtype dtype, gdn2_stream_t stream) {
+  if (tokens < 0 || H <= 0) return GDN2_ERR_INVALID_ARG;
+  if (dtype != GDN2_F32 && dtype != GDN2_BF16) return GDN2_ERR_INVALID_ARG;
+  if (!supported_dv(d_v)) return GDN2_ERR_UNSUPPORTED;
+  if (!fits(tokens, H, d_v, 4)) return GDN2_ERR_INVALID_ARG;
+  if (!norm_weight || !aligned4(norm_weight) || !dnorm_weight || !aligned4(dnorm_weight)) return GDN2_ERR_INVALID_ARG;
+  if ((o_scales != nullptr) != (gate_scales != nullptr)) return GDN2_ERR_INVALID_ARG;
+  if (tokens > 0) {
+    for (const void *p : {o, gate, dy, (const void *)d_o, (const void *)dgate})
+      if (!p || !aligned16(p)) return GDN2_ERR_INVALID_ARG;
+    if (!aligned16(o_scales) || !aligned16(gate_scales)) return GDN2_ERR_INVALID_ARG;
+  }
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (tokens == 0) return finish(cudaMemsetAsync(dnorm_weight, 0, d_v * sizeof(float), s));
+  const gdn2::EpilogueBwdArgs a{o, gate, dy, o_scales, gate_scales, norm_weight, d_o, dgate, dnorm_weight, tokens * H, d_v};
+  return finish(with_workspace(gdn2::epilogue_bwd_workspace_bytes(a.rows, d_v), s,
+                               [&](void *ws) { return gdn2::launch_epilogue_bwd(a, dtype == GDN2_BF16, ws, s); }));
+}
+
+size_t gdn2_block_epilogue_bwd_workspace_bytes(long long tokens, int H, int d_v) {
+  if (tokens <= 0 || H <= 0 || !supported_dv(d_v) || !fits(tokens, H, d_v, 4)) return 0;
+  return gdn2::epilogue_bwd_workspace_bytes(tokens * H, d_v);
+}
+
+gdn2_status gdn2_block_prologue_bwd(const void *x_q, const void *x_k, const void *x_v, const void *x_alpha,
+                                    const void *x_b, const void *x_w, const uint8_t *const *x_scales,
+                                    const float *conv_q, const float *conv_k, const float *conv_v, const void *dq,
+                                    const void *dk, const void *dv, const void *dalpha, const void *db, const void *dw,
+                                    void *dx_q, void *dx_k, void *dx_v, void *dx_alpha, void *dx_b, void *dx_w,
+                                    float *dconv_q, float *dconv_k, float *dconv_v, int B, int T, int H, int d_k,
+                                    int d_v, int conv_len, const int32_t *cu_seqlens, gdn2_dtype dtype,
+                                    gdn2_stream_t stream) {
+  if (B < 0 || T < 0 || H <= 0) return GDN2_ERR_INVALID_ARG;
+  if (dtype != GDN2_F32 && dtype != GDN2_BF16) return GDN2_ERR_INVALID_ARG;
+  if (!supported_dk(d_k) || !supported_dv(d_v) || conv_len < 1 || conv_len > 4) return GDN2_ERR_UNSUPPORTED;
+  const long long tokens = cu_seqlens ? (long long)T : (long long)B * T;
+  // the weight gradients of one run of tokens are indexed with 32 bits
+  if (H > INT_MAX / (4 * 512) || !fits(tokens, H, d_v > d_k ? d_v : d_k, 4)) return GDN2_ERR_INVALID_ARG;
+  for (const float *p : {conv_q, conv_k, conv_v, (const float *)dconv_q, (const float *)dconv_k, (const float *)dconv_v})
+    if (!p || !aligned4(p)) return GDN2_ERR_INVALID_ARG;
+  if (cu_seqlens && !aligned4(cu_seqlens)) return GDN2_ERR_INVALID_ARG;
+  gdn2::PrologueBwdArgs a{{x_q, x_k, x_v, x_alpha, x_b, x_w}, {}, {conv_q, conv_k, conv_v},
+                          {dq, dk, dv, dalpha, db, dw}, {dx_q, dx_k, dx_v, dx_alpha, dx_b, dx_w},
+                          {dconv_q, dconv_k, dconv_v}, cu_seqlens, B, T, H, d_k, d_v, conv_len, tokens};
+  if (tokens > 0)
+    for (int i = 0; i < 6; ++i) {
+      a.scales[i] = x_scales ? x_scales[i] : nullptr;
+      for (const void *p : {a.x[i], a.d[i], (const void *)a.dx[i], x_scales ? (const void *)a.scales[i] : a.x[i]})
+        if (!p || !aligned16(p)) return GDN2_ERR_INVALID_ARG;
+    }
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (B == 0 || tokens == 0) {  // sums over no tokens
+    const size_t col = (size_t)H * conv_len * sizeof(float);
+    cudaError_t err = cudaMemsetAsync(dconv_q, 0, d_k * col, s);
+    if (err == cudaSuccess) err = cudaMemsetAsync(dconv_k, 0, d_k * col, s);
+    if (err == cudaSuccess) err = cudaMemsetAsync(dconv_v, 0, d_v * col, s);
+    return finish(err);
+  }
+  const bool bf16 = dtype == GDN2_BF16;
+  return finish(with_workspace(gdn2::prologue_bwd_workspace_bytes(tokens, H, d_k, d_v, conv_len, bf16), s,
+                               [&](void *ws) { return gdn2::launch_prologue_bwd(a, bf16, ws, s); }));
+}
+
+size_t gdn2_block_prologue_bwd_workspace_bytes(int B, int T, int H, int d_k, int d_v, int conv_len, int packed,
+                                               gdn2_dtype dtype) {
+  if (B <= 0 || T <= 0 || H <= 0 || H > INT_MAX / (4 * 512) || !supported_dk(d_k) || !supported_dv(d_v) ||
+      conv_len < 1 || conv_len > 4 || (dtype != GDN2_F32 && dtype != GDN2_BF16))
+    return 0;
+  const long long tokens = packed ? (long long)T : (long long)B * T;
+  if (!fits(tokens, H, d_v > d_k ? d_v : d_k, 4)) return 0;
+  return gdn2::prologue_bwd_workspace_bytes(tokens, H, d_k, d_v, conv_len, dtype == GDN2_BF16);
 }
 
 }  // extern "C"

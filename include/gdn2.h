@@ -31,8 +31,9 @@
  *     takes a workspace of gdn2_chunk_fwd_workspace_bytes() bytes from a
  *     stream-ordered memory pool that the library creates once per device, and
  *     gives it back on `stream` after its kernels; the pool keeps memory given
- *     back to it for later calls until the process exits.  gdn2_chunk_bwd takes
- *     its workspace from the same pool.  No other call allocates device memory.
+ *     back to it for later calls until the process exits.  gdn2_chunk_bwd,
+ *     gdn2_layer_norm_bwd, gdn2_block_epilogue_bwd and gdn2_block_prologue_bwd take
+ *     their workspaces from the same pool.  No other call allocates device memory.
  *   - Calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy default
  *     stream) and never synchronise.  A validation failure returns before any
  *     launch and writes nothing.  A launch failure returns GDN2_ERR_CUDA.  No
@@ -294,6 +295,123 @@ GDN2_API gdn2_status gdn2_block_prologue(const void *x_q, const void *x_k, const
  */
 GDN2_API gdn2_status gdn2_block_epilogue(const void *o, const void *gate, const float *norm_weight, void *y,
                                          long long tokens, int H, int d_v, gdn2_dtype dtype, gdn2_stream_t stream);
+
+/*
+ * Activations held in 8 bits -- what a training forward keeps for its backward pass.
+ *
+ * They have no counterpart in the pages.  A tensor of `rows` rows of `width` channels is held as
+ *   codes  [rows, width] int8 and scales [rows, ceil(width / 32)] uint8:
+ * for every 32 channels of a row (the last group of a row may be shorter) the least power of two
+ * 2^e, e >= -126, with max |x| <= 127 * 2^e, stored as e + 127; code = x / 2^e rounded to the nearest
+ * integer, ties to even.  The value that is held, code * 2^e, is within 2^(e-1) of x (under 1/126 of
+ * the group's largest value) and exact in fp32 and bf16.  Finite values above 127 * 2^121 are held as
+ * that.  A group holding an infinity or a NaN has
+ * scale 255 and zero codes and reads back as NaN.  33/32 bytes per value.
+ *
+ * gdn2_layer_norm_fwd writes its rows in this form beside its output; gdn2_layer_norm_bwd,
+ * gdn2_block_epilogue_bwd and gdn2_block_prologue_bwd read it in place of the saved activations.
+ *
+ * gdn2_act_pack / gdn2_act_unpack hold and read back `count` (up to GDN2_ACT_MAX_TENSORS) tensors of
+ * one element type in one call.  x, codes, scales, rows and width are HOST arrays of `count` entries
+ * (device pointers, 16-byte aligned, and sizes); they are read before the call returns.  A tensor of
+ * zero rows is skipped (its pointers may be NULL).  Outputs must not overlap inputs or each other.
+ * Asynchronous on `stream`; validation errors return before any launch; more tensors than the limit
+ * are GDN2_ERR_UNSUPPORTED.
+ */
+#define GDN2_ACT_MAX_TENSORS 8
+GDN2_API gdn2_status gdn2_act_pack(const void *const *x, int8_t *const *codes, uint8_t *const *scales,
+                                   const long long *rows, const int *width, int count, gdn2_dtype dtype,
+                                   gdn2_stream_t stream);
+GDN2_API gdn2_status gdn2_act_unpack(const int8_t *const *codes, const uint8_t *const *scales, void *const *x,
+                                     const long long *rows, const int *width, int count, gdn2_dtype dtype,
+                                     gdn2_stream_t stream);
+
+/*
+ * gdn2_layer_norm_fwd -- layer norm of the residual stream, in front of the block's projections.
+ *
+ * The pages name a Transformer-style stack around the block ("NVIDIA AIがGated DeltaNet-2を発表",
+ * ai.warp-studio.com, "アーキテクチャとパフォーマンスベンチマーク") and print no norm for it; this is the
+ * usual one.  For every token, over its `width` channels:
+ *   h = x + residual (rounded to dtype; h = x without a residual),
+ *   mean = sum h / width, rstd = 1 / sqrt(sum (h - mean)^2 / width + eps),
+ *   y = (h - mean) * rstd * weight + bias.
+ *   x, residual, y, h : [tokens, width] (dtype, 16-byte aligned); residual and h are given together
+ *                       or both NULL; h may alias x or residual, y may alias x or residual (not h)
+ *   weight, bias      : [width] fp32, 16-byte aligned; bias may be NULL (zero)
+ *   mean, rstd        : [tokens] fp32 out, both or neither NULL (a forward that is not trained)
+ *   h_codes, h_scales : h held in 8 bits (above) out, both or neither NULL
+ * width: 1 to GDN2_NORM_MAX_WIDTH, anything wider is GDN2_ERR_UNSUPPORTED; rows whose size is a
+ * multiple of 16 bytes move as 16-byte vectors, others value by value.  eps: finite, not negative.
+ * fp32 statistics, the variance about the mean.  Asynchronous on `stream`; allocates nothing.
+ */
+#define GDN2_NORM_MAX_WIDTH 8192
+GDN2_API gdn2_status gdn2_layer_norm_fwd(const void *x, const void *residual, const float *weight, const float *bias,
+                                         float eps, void *y, void *h, float *mean, float *rstd, int8_t *h_codes,
+                                         uint8_t *h_scales, long long tokens, int width, gdn2_dtype dtype,
+                                         gdn2_stream_t stream);
+
+/*
+ * gdn2_layer_norm_bwd -- gradients through gdn2_layer_norm_fwd.  With xh = (h - mean) rstd, e = dy * weight:
+ *   dx = rstd * (e - mean_c(e) - xh * mean_c(e * xh)) + dh      (the gradient of x and of residual alike)
+ *   dweight = sum over tokens of dy * xh,   dbias = sum over tokens of dy
+ *   dy, dx   : [tokens, width] (dtype)      dh : gradient that reaches h past the norm, or NULL (zero)
+ *   h        : [tokens, width] in dtype, or, with h_scales != NULL, its int8 codes (above)
+ *   mean, rstd : as the forward returned them     weight : as in the forward
+ *   dweight, dbias : [width] fp32 out, written (not added to); dbias may be NULL
+ * dx may alias dy or dh.  All sums in fp32 in a fixed order: the results are reproducible on one kind
+ * of device.  Takes gdn2_layer_norm_bwd_workspace_bytes() bytes from the library's pool (partial sums)
+ * and gives them back on `stream`.  Sizes, alignment and errors as for the forward.  tokens == 0
+ * writes zeros to dweight and dbias.
+ */
+GDN2_API gdn2_status gdn2_layer_norm_bwd(const void *dy, const void *h, const uint8_t *h_scales, const float *mean,
+                                         const float *rstd, const float *weight, const void *dh, void *dx,
+                                         float *dweight, float *dbias, long long tokens, int width, gdn2_dtype dtype,
+                                         gdn2_stream_t stream);
+GDN2_API size_t gdn2_layer_norm_bwd_workspace_bytes(long long tokens, int width);
+
+/*
+ * gdn2_block_epilogue_bwd -- gradients through gdn2_block_epilogue.  Per (token, head), with
+ * r = 1 / sqrt(mean(o^2) + 1e-5), oh = o * r, s = SiLU(gate), e = dy * norm_weight * s:
+ *   d_o = r * (e - oh * mean(e * oh)),   dgate = dy * norm_weight * oh * SiLU'(gate),
+ *   dnorm_weight = sum over tokens and heads of dy * oh * s
+ *   o, gate  : the forward's inputs in dtype, or, with o_scales and gate_scales (both or neither),
+ *              their int8 codes (above; groups of 32 channels within a head)
+ *   dy, d_o, dgate : [tokens, H, d_v] (dtype, 16-byte aligned)   dnorm_weight : [d_v] fp32 out, written
+ * d_o and dgate may alias dy, o or gate of the same type (each its own buffer).  fp32 arithmetic and sums, in a fixed order.
+ * Takes gdn2_block_epilogue_bwd_workspace_bytes() bytes from the library's pool.  tokens == 0 writes
+ * zeros to dnorm_weight.  Asynchronous on `stream`; errors as for gdn2_block_epilogue.
+ */
+GDN2_API gdn2_status gdn2_block_epilogue_bwd(const void *o, const void *gate, const uint8_t *o_scales,
+                                             const uint8_t *gate_scales, const float *norm_weight, const void *dy,
+                                             void *d_o, void *dgate, float *dnorm_weight, long long tokens, int H,
+                                             int d_v, gdn2_dtype dtype, gdn2_stream_t stream);
+GDN2_API size_t gdn2_block_epilogue_bwd_workspace_bytes(long long tokens, int H, int d_v);
+
+/*
+ * gdn2_block_prologue_bwd -- gradients through gdn2_block_prologue, from the gradients that
+ * gdn2_chunk_bwd returns.  Per channel, y = conv * x, s = SiLU(y); q and k have n = 1 / sqrt(sum s^2 +
+ * 1e-6) over the head's channels, ds = n dq - n^3 s (s . dq); v has ds = dv; and with dy = ds SiLU'(y):
+ *   dx_t = sum_j conv[c][conv_len-1-j] dy_{t+j},   dconv[c][conv_len-1-j] = sum_t dy_t x_{t-j},
+ * terms inside the sequence only; the gates have dx_alpha = -dalpha p (1 - p), dx_b = db p (1 - p),
+ * dx_w = dw p (1 - p) with p = sigmoid(x).
+ *   x_q .. x_w : the forward's inputs in dtype (x_scales == NULL), or their int8 codes, x_scales then
+ *                being a HOST array of the six scale tensors (above; groups of 32 channels in a head)
+ *   conv_*     : as in the forward        dq .. dw, dx_q .. dx_w : layouts of x_q .. x_w (dtype)
+ *   dconv_q, dconv_k [H * d_k, conv_len], dconv_v [H * d_v, conv_len] : fp32 out, written
+ * Layouts (dense, or packed with cu_seqlens), sizes, alignment and errors as for gdn2_block_prologue;
+ * H at most INT_MAX / 2048.  In a packed batch T may exceed cu_seqlens[B]: the rows behind the last
+ * sequence are not read and their gradients not written.  Outputs must not overlap inputs.  fp32
+ * arithmetic; sums in fp32 in a fixed order.  Takes gdn2_block_prologue_bwd_workspace_bytes() bytes
+ * from the library's pool.  Without tokens (B == 0 or T == 0) zeros go to dconv_*.
+ */
+GDN2_API gdn2_status gdn2_block_prologue_bwd(
+    const void *x_q, const void *x_k, const void *x_v, const void *x_alpha, const void *x_b, const void *x_w,
+    const uint8_t *const *x_scales, const float *conv_q, const float *conv_k, const float *conv_v, const void *dq,
+    const void *dk, const void *dv, const void *dalpha, const void *db, const void *dw, void *dx_q, void *dx_k,
+    void *dx_v, void *dx_alpha, void *dx_b, void *dx_w, float *dconv_q, float *dconv_k, float *dconv_v, int B, int T,
+    int H, int d_k, int d_v, int conv_len, const int32_t *cu_seqlens, gdn2_dtype dtype, gdn2_stream_t stream);
+GDN2_API size_t gdn2_block_prologue_bwd_workspace_bytes(int B, int T, int H, int d_k, int d_v, int conv_len,
+                                                        int packed, gdn2_dtype dtype);
 
 /* Human-readable name of a status; never NULL. */
 GDN2_API const char *gdn2_status_string(gdn2_status status);
