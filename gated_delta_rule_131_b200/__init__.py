@@ -96,7 +96,7 @@ def lib():
         L.gdn2_layer_norm_fwd.restype = ci
         L.gdn2_layer_norm_bwd.argtypes = [vp] * 10 + [cll, ci, ci, vp]
         L.gdn2_layer_norm_bwd.restype = ci
-        L.gdn2_layer_norm_bwd_workspace_bytes.argtypes = [cll, ci]
+        L.gdn2_layer_norm_bwd_workspace_bytes.argtypes = [cll, ci, ci]
         L.gdn2_layer_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
         L.gdn2_block_epilogue_bwd.argtypes = [vp] * 9 + [cll, ci, ci, ci, vp]
         L.gdn2_block_epilogue_bwd.restype = ci
@@ -391,63 +391,91 @@ class LayerNormOut(NamedTuple):
     checkpoint: Optional[Act8]
 
 
-@contextlib.contextmanager
-def _launching(stream, *tensors):
-    """The device of ``tensors`` and the launch stream made current: outputs are allocated for that
-    stream, and inputs are kept until its work is done.  Yields the stream's handle."""
-    tensors = [t for t in tensors if t is not None]
-    _check_tensors(*tensors)
-    dev = tensors[0].device
-    with torch.cuda.device(dev):
-        own = torch.cuda.current_stream(dev)
-        if stream is None or stream == own:
-            yield _stream(own)
-            return
-        if stream.device != dev:
+class _launching:
+    """Makes the device of ``tensors`` and the launch stream current: outputs are allocated for that
+    stream, and inputs are kept until its work is done.  Enters with the stream's handle."""
+    __slots__ = ("tensors", "stream", "guards")
+
+    def __init__(self, stream, *tensors):
+        self.tensors, self.stream, self.guards = tensors, stream, None
+
+    def __enter__(self):
+        dev = None
+        for t in self.tensors:
+            if t is None:
+                continue
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("gdn2: all tensors must be CUDA tensors")
+            if dev is None:
+                dev = d
+            elif d != dev:
+                raise ValueError("gdn2: tensors on different devices")
+            if not t.is_contiguous():
+                raise ValueError("gdn2: all tensors must be contiguous")
+        if self.stream is None and dev == torch.cuda.current_device():  # nothing to switch
+            return torch._C._cuda_getCurrentRawStream(dev)
+        self.guards = contextlib.ExitStack()
+        self.guards.enter_context(torch.cuda.device(dev))
+        if self.stream is None or self.stream == torch.cuda.current_stream(dev):
+            self.stream = None
+        elif self.stream.device.index != dev:
+            self.guards.close()
             raise ValueError("gdn2: the stream is on another device than the tensors")
-        with torch.cuda.stream(stream):
-            yield _stream(stream)
-        for t in tensors:
-            t.record_stream(stream)
+        else:
+            self.guards.enter_context(torch.cuda.stream(self.stream))
+        return torch._C._cuda_getCurrentRawStream(dev)
+
+    def __exit__(self, *exc):
+        if self.guards is not None:
+            self.guards.close()
+            if self.stream is not None:
+                for t in self.tensors:
+                    if t is not None:
+                        t.record_stream(self.stream)
+        return False
 
 
-def _shapes(what, expect, **tensors):
-    for name, t in tensors.items():
-        if t is not None and tuple(t.shape) != tuple(expect):
-            raise ValueError(f"gdn2: {what}: {name} has shape {tuple(t.shape)}, expected {tuple(expect)}")
+def _expect(what, name, t, dtype, shape):
+    if t is None or (t.dtype is dtype and t.shape == shape):
+        return
+    raise ValueError(f"gdn2: {what}: {name} must be {dtype} of shape {tuple(shape)}, not {t.dtype} of {tuple(t.shape)}")
 
 
-def _types(what, dtype, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != dtype:
-            raise ValueError(f"gdn2: {what}: {name} must be {dtype}")
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _act8_shape(shape):
+    return (*shape[:-1], -(-shape[-1] // ACT_GROUP))
 
 
 def _check_act8(what, name, a, shape):
-    _types(what, torch.int8, **{name + ".codes": a.codes})
-    _types(what, torch.uint8, **{name + ".scales": a.scales})
-    _shapes(what, shape, **{name + ".codes": a.codes})
-    _shapes(what, tuple(shape[:-1]) + (-(-shape[-1] // ACT_GROUP),), **{name + ".scales": a.scales})
+    _expect(what, name + ".codes", a.codes, torch.int8, shape)
+    _expect(what, name + ".scales", a.scales, torch.uint8, _act8_shape(shape))
 
 
-def _new_act8(shape, device):
-    return Act8(torch.empty(shape, dtype=torch.int8, device=device),
-                torch.empty(tuple(shape[:-1]) + (-(-shape[-1] // ACT_GROUP),), dtype=torch.uint8, device=device))
+def _new_act8(x):
+    return Act8(torch.empty_like(x, dtype=torch.int8), x.new_empty(_act8_shape(x.shape), dtype=torch.uint8))
 
 
-def _rows(shape):
-    n = 1
-    for s in shape[:-1]:
-        n *= s
-    return n
+def _saved(what, name, x, like):
+    """A saved activation as (values or codes, scales or None), checked against its gradient."""
+    if isinstance(x, Act8):
+        _check_act8(what, name, x, like.shape)
+        return x.codes, x.scales
+    _expect(what, name, x, like.dtype, like.shape)
+    return x, None
 
 
-def _act_call(entry, first, second, third, shapes, dtype, stream):
-    n = len(shapes)
-    ptrs = [(ctypes.c_void_p * n)(*[t.data_ptr() for t in ts]) for ts in (first, second, third)]
-    rows = (ctypes.c_longlong * n)(*[_rows(s) for s in shapes])
-    width = (ctypes.c_int * n)(*[s[-1] for s in shapes])
-    st = getattr(lib(), entry)(*ptrs, rows, width, n, _DTYPES[dtype], stream)
+def _act_call(entry, first, second, third, shaped, dtype, stream):
+    n = len(shaped)
+    vps = ctypes.c_void_p * n
+    width = [t.shape[-1] for t in shaped]
+    st = getattr(lib(), entry)(vps(*[t.data_ptr() for t in first]), vps(*[t.data_ptr() for t in second]),
+                               vps(*[t.data_ptr() for t in third]),
+                               (ctypes.c_longlong * n)(*[t.numel() // w for t, w in zip(shaped, width)]),
+                               (ctypes.c_int * n)(*width), n, _DTYPES[dtype], stream)
     if st != GDN2_OK:
         raise Gdn2Error(st, entry)
 
@@ -459,14 +487,15 @@ def act_pack(xs, stream=None):
     xs = [xs] if one else list(xs)
     if not xs:
         return []
-    if xs[0].dtype not in _DTYPES or any(x.dtype != xs[0].dtype for x in xs):
-        raise ValueError("gdn2: act_pack: the tensors must share dtype float32 or bfloat16")
-    if any(x.dim() < 1 or x.shape[-1] < 1 for x in xs):
-        raise ValueError("gdn2: act_pack: a tensor needs a last dimension of at least 1")
+    dtype = xs[0].dtype
+    for x in xs:
+        if x.dtype is not dtype or dtype not in _DTYPES:
+            raise ValueError("gdn2: act_pack: the tensors must share dtype float32 or bfloat16")
+        if x.dim() < 1 or x.shape[-1] < 1:
+            raise ValueError("gdn2: act_pack: a tensor needs a last dimension of at least 1")
     with _launching(stream, *xs) as s:
-        out = [_new_act8(x.shape, x.device) for x in xs]
-        _act_call("gdn2_act_pack", xs, [a.codes for a in out], [a.scales for a in out], [x.shape for x in xs],
-                  xs[0].dtype, s)
+        out = [_new_act8(x) for x in xs]
+        _act_call("gdn2_act_pack", xs, [a.codes for a in out], [a.scales for a in out], xs, dtype, s)
     return out[0] if one else out
 
 
@@ -482,10 +511,10 @@ def act_unpack(acts, dtype=torch.bfloat16, stream=None):
         if a.codes.dim() < 1 or a.codes.shape[-1] < 1:
             raise ValueError("gdn2: act_unpack: a tensor needs a last dimension of at least 1")
         _check_act8("act_unpack", "act", a, a.codes.shape)
-    with _launching(stream, *[t for a in acts for t in a]) as s:
-        out = [torch.empty(a.codes.shape, dtype=dtype, device=a.codes.device) for a in acts]
-        _act_call("gdn2_act_unpack", [a.codes for a in acts], [a.scales for a in acts], out, [x.shape for x in out],
-                  dtype, s)
+    codes, scales = [a.codes for a in acts], [a.scales for a in acts]
+    with _launching(stream, *codes, *scales) as s:
+        out = [torch.empty_like(c, dtype=dtype) for c in codes]
+        _act_call("gdn2_act_unpack", codes, scales, out, out, dtype, s)
     return out[0] if one else out
 
 
@@ -496,24 +525,29 @@ def layer_norm_fwd(x, weight, bias=None, residual=None, eps=1e-5, checkpoint=Fal
     with ``stats=False``; ``checkpoint=True`` also returns ``h`` held in 8 bits.  See
     ``gdn2_layer_norm_fwd`` in ``include/gdn2.h``.
     """
-    if x.dtype not in _DTYPES:
+    what, shape, dtype = "layer_norm_fwd", x.shape, x.dtype
+    if dtype not in _DTYPES:
         raise ValueError("gdn2: layer_norm_fwd: x must be float32 or bfloat16")
-    if x.dim() < 1 or x.shape[-1] < 1:
+    if not shape or shape[-1] < 1:
         raise ValueError("gdn2: layer_norm_fwd: x needs a last dimension of at least 1")
-    D = x.shape[-1]
-    _types("layer_norm_fwd", x.dtype, residual=residual)
-    _types("layer_norm_fwd", torch.float32, weight=weight, bias=bias)
-    _shapes("layer_norm_fwd", x.shape, residual=residual)
-    _shapes("layer_norm_fwd", (D,), weight=weight, bias=bias)
+    D = shape[-1]
+    _expect(what, "residual", residual, dtype, shape)
+    _expect(what, "weight", weight, torch.float32, (D,))
+    _expect(what, "bias", bias, torch.float32, (D,))
     with _launching(stream, x, weight, bias, residual) as s:
         y = torch.empty_like(x)
-        h = None if residual is None else torch.empty_like(x)
-        mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if stats else None
-                      for _ in range(2))
-        ck = _new_act8(x.shape, x.device) if checkpoint else None
-        st = lib().gdn2_layer_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(h),
-                                       _ptr(mean), _ptr(rstd), *([_ptr(t) for t in ck] if ck else (None, None)),
-                                       _rows(x.shape), D, _DTYPES[x.dtype], s)
+        h = mean = rstd = ck = codes = scales = None
+        if residual is not None:
+            h = torch.empty_like(x)
+        if stats:
+            mean = x.new_empty(shape[:-1], dtype=torch.float32)
+            rstd = torch.empty_like(mean)
+        if checkpoint:
+            ck = _new_act8(x)
+            codes, scales = ck
+        st = lib().gdn2_layer_norm_fwd(x.data_ptr(), _addr(residual), weight.data_ptr(), _addr(bias), eps, y.data_ptr(),
+                                       _addr(h), _addr(mean), _addr(rstd), _addr(codes), _addr(scales), x.numel() // D,
+                                       D, _DTYPES[dtype], s)
         if st != GDN2_OK:
             raise Gdn2Error(st, "gdn2_layer_norm_fwd")
     return LayerNormOut(y, x if h is None else h, mean, rstd, ck)
@@ -526,42 +560,31 @@ def layer_norm_bwd(dy, h, mean, rstd, weight, dh=None, want_dbias=True, stream=N
     ``h`` is the forward's ``h`` or its :class:`Act8` checkpoint.  ``dbias`` is None unless
     ``want_dbias``.  See ``gdn2_layer_norm_bwd`` in ``include/gdn2.h``.
     """
-    if dy.dtype not in _DTYPES:
+    what, shape, dtype = "layer_norm_bwd", dy.shape, dy.dtype
+    if dtype not in _DTYPES:
         raise ValueError("gdn2: layer_norm_bwd: dy must be float32 or bfloat16")
-    if dy.dim() < 1 or dy.shape[-1] < 1:
+    if not shape or shape[-1] < 1:
         raise ValueError("gdn2: layer_norm_bwd: dy needs a last dimension of at least 1")
-    D = dy.shape[-1]
-    _types("layer_norm_bwd", dy.dtype, dh=dh)
-    _types("layer_norm_bwd", torch.float32, mean=mean, rstd=rstd, weight=weight)
-    _shapes("layer_norm_bwd", dy.shape, dh=dh)
-    _shapes("layer_norm_bwd", dy.shape[:-1], mean=mean, rstd=rstd)
-    _shapes("layer_norm_bwd", (D,), weight=weight)
-    codes, scales = _saved("layer_norm_bwd", "h", h, dy)
-    with _launching(stream, dy, codes, scales, mean, rstd, weight, dh) as s:
-        dx = torch.empty_like(dy)
-        dweight = torch.empty(D, dtype=torch.float32, device=dy.device)
-        dbias = torch.empty_like(dweight) if want_dbias else None
-        st = lib().gdn2_layer_norm_bwd(_ptr(dy), _ptr(codes), _ptr(scales), _ptr(mean), _ptr(rstd), _ptr(weight),
-                                       _ptr(dh), _ptr(dx), _ptr(dweight), _ptr(dbias), _rows(dy.shape), D,
-                                       _DTYPES[dy.dtype], s)
+    D = shape[-1]
+    _expect(what, "dh", dh, dtype, shape)
+    _expect(what, "mean", mean, torch.float32, shape[:-1])
+    _expect(what, "rstd", rstd, torch.float32, shape[:-1])
+    _expect(what, "weight", weight, torch.float32, (D,))
+    values, scales = _saved(what, "h", h, dy)
+    with _launching(stream, dy, values, scales, mean, rstd, weight, dh) as s:
+        dx, dweight = torch.empty_like(dy), torch.empty_like(weight)
+        dbias = torch.empty_like(weight) if want_dbias else None
+        st = lib().gdn2_layer_norm_bwd(dy.data_ptr(), values.data_ptr(), _addr(scales), mean.data_ptr(),
+                                       rstd.data_ptr(), weight.data_ptr(), _addr(dh), dx.data_ptr(),
+                                       dweight.data_ptr(), _addr(dbias), dy.numel() // D, D, _DTYPES[dtype], s)
         if st != GDN2_OK:
             raise Gdn2Error(st, "gdn2_layer_norm_bwd")
     return dx, dweight, dbias
 
 
-def _saved(what, name, x, like):
-    """A saved activation as (values or codes, scales or None), checked against its gradient."""
-    if isinstance(x, Act8):
-        _check_act8(what, name, x, like.shape)
-        return x.codes, x.scales
-    _types(what, like.dtype, **{name: x})
-    _shapes(what, like.shape, **{name: x})
-    return x, None
-
-
-def layer_norm_bwd_workspace_bytes(tokens, width) -> int:
+def layer_norm_bwd_workspace_bytes(tokens, width, dtype=torch.bfloat16) -> int:
     """Device bytes ``layer_norm_bwd`` takes from the library's pool for this shape."""
-    return int(lib().gdn2_layer_norm_bwd_workspace_bytes(tokens, width))
+    return int(lib().gdn2_layer_norm_bwd_workspace_bytes(tokens, width, _DTYPES[dtype]))
 
 
 def block_epilogue_bwd(o, gate, norm_weight, dy, stream=None):
@@ -570,23 +593,22 @@ def block_epilogue_bwd(o, gate, norm_weight, dy, stream=None):
     ``o`` and ``gate`` are the forward's inputs, or both :class:`Act8` checkpoints of them.  See
     ``gdn2_block_epilogue_bwd`` in ``include/gdn2.h``.
     """
-    if dy.dtype not in _DTYPES:
+    what, shape, dtype = "block_epilogue_bwd", dy.shape, dy.dtype
+    if dtype not in _DTYPES:
         raise ValueError("gdn2: block_epilogue_bwd: dy must be float32 or bfloat16")
-    if dy.dim() < 2:
+    if len(shape) < 2 or shape[-2] < 1 or shape[-1] < 1:
         raise ValueError("gdn2: block_epilogue_bwd: dy must be [..., H, d_v]")
     if isinstance(o, Act8) != isinstance(gate, Act8):
         raise ValueError("gdn2: block_epilogue_bwd: o and gate are both tensors or both Act8")
-    H, dv = dy.shape[-2], dy.shape[-1]
-    _types("block_epilogue_bwd", torch.float32, norm_weight=norm_weight)
-    _shapes("block_epilogue_bwd", (dv,), norm_weight=norm_weight)
-    oc, osc = _saved("block_epilogue_bwd", "o", o, dy)
-    gc, gsc = _saved("block_epilogue_bwd", "gate", gate, dy)
+    H, dv = shape[-2], shape[-1]
+    _expect(what, "norm_weight", norm_weight, torch.float32, (dv,))
+    oc, osc = _saved(what, "o", o, dy)
+    gc, gsc = _saved(what, "gate", gate, dy)
     with _launching(stream, oc, osc, gc, gsc, norm_weight, dy) as s:
-        do, dgate = torch.empty_like(dy), torch.empty_like(dy)
-        dnorm_weight = torch.empty(dv, dtype=torch.float32, device=dy.device)
-        st = lib().gdn2_block_epilogue_bwd(_ptr(oc), _ptr(gc), _ptr(osc), _ptr(gsc), _ptr(norm_weight), _ptr(dy),
-                                           _ptr(do), _ptr(dgate), _ptr(dnorm_weight), _rows(dy.shape[:-1]), H, dv,
-                                           _DTYPES[dy.dtype], s)
+        do, dgate, dnorm_weight = torch.empty_like(dy), torch.empty_like(dy), torch.empty_like(norm_weight)
+        st = lib().gdn2_block_epilogue_bwd(oc.data_ptr(), gc.data_ptr(), _addr(osc), _addr(gsc), norm_weight.data_ptr(),
+                                           dy.data_ptr(), do.data_ptr(), dgate.data_ptr(), dnorm_weight.data_ptr(),
+                                           dy.numel() // (H * dv), H, dv, _DTYPES[dtype], s)
         if st != GDN2_OK:
             raise Gdn2Error(st, "gdn2_block_epilogue_bwd")
     return do, dgate, dnorm_weight
@@ -595,6 +617,9 @@ def block_epilogue_bwd(o, gate, norm_weight, dy, stream=None):
 def block_epilogue_bwd_workspace_bytes(tokens, H, d_v) -> int:
     """Device bytes ``block_epilogue_bwd`` takes from the library's pool for this shape."""
     return int(lib().gdn2_block_epilogue_bwd_workspace_bytes(tokens, H, d_v))
+
+
+_PRE = ("xq", "xk", "xv", "xa", "xb", "xw")
 
 
 def block_prologue_bwd(xq, xk, xv, xa, xb, xw, conv_q, conv_k, conv_v, dq, dk, dv, dalpha, db, dw, cu_seqlens=None,
@@ -606,39 +631,47 @@ def block_prologue_bwd(xq, xk, xv, xa, xb, xw, conv_q, conv_k, conv_v, dq, dk, d
     rows behind the last sequence keep whatever memory their gradients were given.  See
     ``gdn2_block_prologue_bwd`` in ``include/gdn2.h``.
     """
-    what = "block_prologue_bwd"
+    what, shape, dtype = "block_prologue_bwd", dq.shape, dq.dtype
     xs, grads, convs = (xq, xk, xv, xa, xb, xw), (dq, dk, dv, dalpha, db, dw), (conv_q, conv_k, conv_v)
-    if dq.dtype not in _DTYPES or any(g.dtype != dq.dtype for g in grads):
-        raise ValueError("gdn2: block_prologue_bwd: the gradients must share dtype float32 or bfloat16")
+    if dtype not in _DTYPES:
+        raise ValueError("gdn2: block_prologue_bwd: the gradients must be float32 or bfloat16")
     packed8 = isinstance(xq, Act8)
-    if any(isinstance(x, Act8) != packed8 for x in xs):
-        raise ValueError("gdn2: block_prologue_bwd: the saved inputs are all tensors or all Act8")
-    if dq.dim() != (4 if cu_seqlens is None else 3):
-        raise ValueError("gdn2: block_prologue_bwd: gradients are [B, T, H, d], or [T, H, d] with cu_seqlens")
+    for x in xs:
+        if isinstance(x, Act8) != packed8:
+            raise ValueError("gdn2: block_prologue_bwd: the saved inputs are all tensors or all Act8")
+    if len(shape) != (4 if cu_seqlens is None else 3) or not dv.shape or conv_q.dim() != 2:
+        raise ValueError("gdn2: block_prologue_bwd: gradients are [B, T, H, d], or [T, H, d] with cu_seqlens; "
+                         "convolution weights [H * d, K]")
     if cu_seqlens is None:
-        B, T, H, d_k = dq.shape
+        B, T, H, d_k = shape
     else:
-        _types(what, torch.int32, cu_seqlens=cu_seqlens)
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError("gdn2: block_prologue_bwd: cu_seqlens must be [B + 1]")
+        if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("gdn2: block_prologue_bwd: cu_seqlens must be int32 [B + 1]")
         B = cu_seqlens.numel() - 1
-        T, H, d_k = dq.shape
-    d_v = dv.shape[-1]
-    K = conv_q.shape[-1]
-    _shapes(what, dq.shape, dk=dk, dalpha=dalpha, db=db)
-    _shapes(what, tuple(dq.shape[:-1]) + (d_v,), dv=dv, dw=dw)
-    _types(what, torch.float32, conv_q=conv_q, conv_k=conv_k, conv_v=conv_v)
-    _shapes(what, (H * d_k, K), conv_q=conv_q, conv_k=conv_k)
-    _shapes(what, (H * d_v, K), conv_v=conv_v)
-    saved = [_saved(what, n, x, g) for n, x, g in zip(("xq", "xk", "xv", "xa", "xb", "xw"), xs, grads)]
-    with _launching(stream, *grads, *[t for pair in saved for t in pair], *convs, cu_seqlens) as s:
-        dxs = [torch.empty_like(g) for g in grads]
-        dconv = [torch.empty_like(c) for c in convs]
-        scales = (ctypes.c_void_p * 6)(*[sc.data_ptr() for _, sc in saved]) if packed8 else None
-        st = lib().gdn2_block_prologue_bwd(*[_ptr(c) for c, _ in saved], scales, *[_ptr(c) for c in convs],
-                                           *[_ptr(g) for g in grads], *[_ptr(t) for t in dxs],
-                                           *[_ptr(t) for t in dconv], B, T, H, d_k, d_v, K, _ptr(cu_seqlens),
-                                           _DTYPES[dq.dtype], s)
+        T, H, d_k = shape
+    d_v, K = dv.shape[-1], conv_q.shape[1]
+    vshape = (*shape[:-1], d_v)
+    for name, t, expect in zip(("dq", "dk", "dv", "dalpha", "db", "dw"), grads,
+                               (shape, shape, vshape, shape, shape, vshape)):
+        _expect(what, name, t, dtype, expect)
+    for name, t, d in zip(("conv_q", "conv_k", "conv_v"), convs, (d_k, d_k, d_v)):
+        _expect(what, name, t, torch.float32, (H * d, K))
+    if packed8:
+        for name, x, t in zip(_PRE, xs, grads):
+            _check_act8(what, name, x, t.shape)
+        saved, scale_list = [x.codes for x in xs], [x.scales for x in xs]
+    else:
+        for name, x, t in zip(_PRE, xs, grads):
+            _expect(what, name, x, dtype, t.shape)
+        saved, scale_list = xs, ()
+    with _launching(stream, *grads, *saved, *scale_list, *convs, cu_seqlens) as s:
+        dxs = [torch.empty_like(t) for t in grads]
+        dconv = [torch.empty_like(t) for t in convs]
+        scales = (ctypes.c_void_p * 6)(*[t.data_ptr() for t in scale_list]) if packed8 else None
+        st = lib().gdn2_block_prologue_bwd(*[t.data_ptr() for t in saved], scales, *[t.data_ptr() for t in convs],
+                                           *[t.data_ptr() for t in grads], *[t.data_ptr() for t in dxs],
+                                           *[t.data_ptr() for t in dconv], B, T, H, d_k, d_v, K, _addr(cu_seqlens),
+                                           _DTYPES[dtype], s)
         if st != GDN2_OK:
             raise Gdn2Error(st, "gdn2_block_prologue_bwd")
     return (*dxs, *dconv)

@@ -3,6 +3,7 @@
 //
 // Packing and unpacking are HBM-bound streams: each value is read once and written once.
 #include <algorithm>
+#include <atomic>
 
 #include "act8.cuh"
 
@@ -12,33 +13,33 @@ namespace {
 constexpr int NU = 4;  // vectors that a lane has in flight
 
 // Rows whose width is a multiple of 32: groups lie end to end over the whole tensor, so a lane's
-// vector index needs no row.  One tensor per grid row.
+// vector index needs no row.  A block takes tiles of 256 * NU vectors; one tensor per grid row.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) act_pack_flat_kernel(const ActArgs a) {
-  const ActTensor t = a.t[blockIdx.y];
+  constexpr int LPG = ACT_GROUP / VEC;
+  const ActTensor &t = a.t[blockIdx.y];
   const long long nvec = t.rows * t.width / VEC;  // a multiple of the lanes of a group
-  const LaneVec<T, VEC> *x = static_cast<const LaneVec<T, VEC> *>(t.x);
-  LaneVec<int8_t, VEC> *c = reinterpret_cast<LaneVec<int8_t, VEC> *>(t.codes);
   for (long long b = (long long)blockIdx.x * (256 * NU); b < nvec; b += (long long)gridDim.x * (256 * NU)) {
+    const T *x = static_cast<const T *>(t.x) + b * VEC;
+    int8_t *codes = t.codes + b * VEC;
+    uint8_t *scales = t.scales + b / LPG;
+    const int n = (int)min(nvec - b, (long long)(256 * NU));
     LaneVec<T, VEC> r[NU];
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const long long i = b + u * 256 + threadIdx.x;
-      if (i < nvec) r[u] = x[i];
+      const int i = u * 256 + threadIdx.x;
+      if (i < n) r[u].load(x + i * VEC);
     }
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const long long i = b + u * 256 + threadIdx.x;
-      float f[VEC];
-      widen(r[u], f);
-      if (i >= nvec)
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) f[k] = 0.f;
+      const int i = u * 256 + threadIdx.x;
+      Pairs<VEC> f;
+      widen<0, VEC>(r[u], f);
       uint32_t s;
-      const LaneVec<int8_t, VEC> v = act8_encode<VEC>(f, s);
-      if (i < nvec) {
-        c[i] = v;
-        if (i % (ACT_GROUP / VEC) == 0) t.scales[i / (ACT_GROUP / VEC)] = (uint8_t)s;
+      const LaneVec<int8_t, VEC> v = act8_encode<0>(r[u], f, i < n, s);
+      if (i < n) {
+        v.store(codes + i * VEC);
+        if (i % LPG == 0) scales[i / LPG] = (uint8_t)s;
       }
     }
   }
@@ -46,30 +47,33 @@ __global__ void __launch_bounds__(256) act_pack_flat_kernel(const ActArgs a) {
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) act_unpack_flat_kernel(const ActArgs a) {
-  const ActTensor t = a.t[blockIdx.y];
+  constexpr int LPG = ACT_GROUP / VEC;
+  const ActTensor &t = a.t[blockIdx.y];
   const long long nvec = t.rows * t.width / VEC;
-  const LaneVec<int8_t, VEC> *c = reinterpret_cast<const LaneVec<int8_t, VEC> *>(t.codes);
-  LaneVec<T, VEC> *x = static_cast<LaneVec<T, VEC> *>(t.x);
   for (long long b = (long long)blockIdx.x * (256 * NU); b < nvec; b += (long long)gridDim.x * (256 * NU)) {
+    const int8_t *codes = t.codes + b * VEC;
+    const uint8_t *scales = t.scales + b / LPG;
+    T *x = static_cast<T *>(t.x) + b * VEC;
+    const int n = (int)min(nvec - b, (long long)(256 * NU));
     LaneVec<int8_t, VEC> r[NU];
     uint32_t s[NU];
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const long long i = b + u * 256 + threadIdx.x;
-      if (i < nvec) {
-        r[u] = c[i];
-        s[u] = t.scales[i / (ACT_GROUP / VEC)];
+      const int i = u * 256 + threadIdx.x;
+      if (i < n) {
+        r[u].load(codes + i * VEC);
+        s[u] = scales[i / LPG];
       }
     }
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const long long i = b + u * 256 + threadIdx.x;
-      if (i < nvec) {
-        float f[VEC];
-        widen(r[u], act8_unit(s[u]), f);
+      const int i = u * 256 + threadIdx.x;
+      if (i < n) {
+        Pairs<VEC> f;
+        widen<0, VEC>(r[u], act8_unit(s[u]), f);
         LaneVec<T, VEC> v;
-        narrow(f, v);
-        x[i] = v;
+        narrow<0, VEC>(f, v);
+        v.store(x + i * VEC);
       }
     }
   }
@@ -79,7 +83,7 @@ __global__ void __launch_bounds__(256) act_unpack_flat_kernel(const ActArgs a) {
 template <typename T, int VEC, bool PACK>
 __global__ void __launch_bounds__(256) act_rows_kernel(const ActArgs a) {
   constexpr int SPAN = 32 * VEC * NU;
-  const ActTensor t = a.t[blockIdx.y];
+  const ActTensor &t = a.t[blockIdx.y];
   const int per_row = (t.width + SPAN - 1) / SPAN, lane = threadIdx.x & 31;
   const int groups = (t.width + ACT_GROUP - 1) / ACT_GROUP;
   const long long tasks = t.rows * per_row, step = (long long)gridDim.x * 8;
@@ -97,9 +101,9 @@ __global__ void __launch_bounds__(256) act_rows_kernel(const ActArgs a) {
       const int c = c0 + u * 32 * VEC;  // VEC divides the width: a vector is inside the row or outside
       if (c < t.width) {
         if constexpr (PACK) {
-          r[u] = *reinterpret_cast<const LaneVec<T, VEC> *>(x + c);
+          r[u].load(x + c);
         } else {
-          q[u] = *reinterpret_cast<const LaneVec<int8_t, VEC> *>(codes + c);
+          q[u].load(codes + c);
           s[u] = scales[c / ACT_GROUP];
         }
       }
@@ -107,23 +111,20 @@ __global__ void __launch_bounds__(256) act_rows_kernel(const ActArgs a) {
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       const int c = c0 + u * 32 * VEC;
-      float f[VEC];
+      Pairs<VEC + VEC % 2> f;
       if constexpr (PACK) {
-        widen(r[u], f);
-        if (c >= t.width)
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) f[i] = 0.f;
+        widen<0, VEC>(r[u], f);
         uint32_t sc;
-        const LaneVec<int8_t, VEC> v = act8_encode<VEC>(f, sc);
+        const LaneVec<int8_t, VEC> v = act8_encode<0>(r[u], f, c < t.width, sc);
         if (c < t.width) {
-          *reinterpret_cast<LaneVec<int8_t, VEC> *>(codes + c) = v;
+          v.store(codes + c);
           if (c % ACT_GROUP == 0) scales[c / ACT_GROUP] = (uint8_t)sc;
         }
       } else if (c < t.width) {
-        widen(q[u], act8_unit(s[u]), f);
+        widen<0, VEC>(q[u], act8_unit(s[u]), f);
         LaneVec<T, VEC> v;
-        narrow(f, v);
-        *reinterpret_cast<LaneVec<T, VEC> *>(x + c) = v;
+        narrow<0, VEC>(f, v);
+        v.store(x + c);
       }
     }
   }
@@ -163,24 +164,28 @@ cudaError_t act_t(const ActArgs &all, cudaStream_t stream) {
   return cudaSuccess;
 }
 
-// A block sums 32 columns: warp w takes the rows w, w + 8, ... (lane = column), then the eight warps'
-// sums are added in order.
-__global__ void __launch_bounds__(256) colsum_kernel(const ColSumArgs a) {
-  __shared__ float part[8][33];
+// A block sums 32 columns (lane = column): warp w takes the rows w, w + W, ... of its W warps, eight
+// loads in flight and added as a tree, then the first warp adds the warps' sums in order.
+constexpr int SUM_WARPS = 32;
+__global__ void __launch_bounds__(32 * SUM_WARPS) colsum_kernel(const ColSumArgs a) {
+  __shared__ float part[SUM_WARPS][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (col < a.ncols) {
     const float *p = a.parts + col;
-#pragma unroll 8
-    for (int r = warp; r < a.nparts; r += 8) s += p[(size_t)r * a.ncols];
+    for (int r = warp; r < a.nparts; r += 8 * W) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = r + i * W < a.nparts ? p[(size_t)(r + i * W) * a.ncols] : 0.f;
+      s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
   }
   part[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && col < a.ncols) {
-#pragma unroll
-    for (int w = 1; w < 8; ++w) s += part[w][lane];
+    for (int w = 1; w < W; ++w) s += part[w][lane];
     const int k = col < a.end[0] ? 0 : col < a.end[1] ? 1 : 2;
     if (a.out[k]) a.out[k][col - (k ? a.end[k - 1] : 0)] = s;
   }
@@ -189,13 +194,30 @@ __global__ void __launch_bounds__(256) colsum_kernel(const ColSumArgs a) {
 }  // namespace
 
 int sm_count() {
+  static std::atomic<int> known[64];  // by device; 0: not asked yet
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      sms <= 0) {
-    cudaGetLastError();  // no device: the sizes below are host arithmetic only
-    sms = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();  // no device: the sizes are host arithmetic only
+    return 148;
   }
+  if ((sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+    cudaGetLastError();
+    return 148;
+  }
+  known[dev].store(sms, std::memory_order_relaxed);
   return sms;
+}
+
+cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &devices) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (devices.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess) devices.fetch_or(bit, std::memory_order_relaxed);
+  return err;
 }
 
 cudaError_t launch_colsum(const ColSumArgs &a, cudaStream_t stream) {
@@ -204,7 +226,7 @@ cudaError_t launch_colsum(const ColSumArgs &a, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)((a.ncols + 31) / 32));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(32 * std::min(SUM_WARPS, (a.nparts + 7) / 8));  // one round of eight loads, or more
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

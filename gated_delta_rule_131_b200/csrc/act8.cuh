@@ -10,6 +10,8 @@
 // holds an infinity or a NaN has the scale byte 255 and zero codes, and reads back as NaN.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace gdn2 {
@@ -27,135 +29,193 @@ __device__ __forceinline__ float act8_inverse(uint32_t s) { return s == 255u ? 0
 // The scale itself; +inf for the NaN scale, which the zero codes turn into NaN.
 __device__ __forceinline__ float act8_unit(uint32_t s) { return __uint_as_float(s << 23); }
 
-// x / scale rounded to an integer in the low byte: adding 1.5 * 2^23 leaves the integer part in the
-// last mantissa bits, rounded once by the fused multiply-add, ties to even.
-__device__ __forceinline__ uint32_t act8_round(float x, float inv) {
-  return __float_as_uint(fmaf(x, inv, 12582912.f));
-}
-__device__ __forceinline__ uint32_t act8_code4(const float *x, float inv) {
-  const uint32_t lo = __byte_perm(act8_round(x[0], inv), act8_round(x[1], inv), 0x0040);
-  const uint32_t hi = __byte_perm(act8_round(x[2], inv), act8_round(x[3], inv), 0x0040);
-  return __byte_perm(lo, hi, 0x5410);
-}
-// Four codes of a word times their unit: each byte (offset by 128) becomes the low mantissa byte of
-// 2^23 + 128 + code; the difference and the product are exact.
-__device__ __forceinline__ void act8_value4(uint32_t w, float unit, float *x) {
-  const uint32_t o = w ^ 0x80808080u;
+// N values as fp32 pairs: sums, products and fused multiply-adds run two to an instruction.
+template <int N> struct Pairs {
+  static_assert(N % 2 == 0, "whole pairs");
+  float2 p[N / 2];
+  __device__ __forceinline__ float get(int i) const { return i & 1 ? p[i >> 1].y : p[i >> 1].x; }
+  __device__ __forceinline__ void set(int i, float v) { (i & 1 ? p[i >> 1].y : p[i >> 1].x) = v; }
+};
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+template <int N> __device__ __forceinline__ void fill(Pairs<N> &a, float x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    x[i] = (__uint_as_float(__byte_perm(o, 0x4b000000u, 0x7440 + i)) - 8388736.f) * unit;
+  for (int i = 0; i < N / 2; ++i) a.p[i] = splat(x);
+}
+template <int N> __device__ __forceinline__ float total(const Pairs<N> &a) {
+  float2 s = a.p[0];
+#pragma unroll
+  for (int i = 1; i < N / 2; ++i) s = __fadd2_rn(s, a.p[i]);
+  return s.x + s.y;
+}
+template <int N> __device__ __forceinline__ float dot(const Pairs<N> &a, const Pairs<N> &b) {
+  float2 s = __fmul2_rn(a.p[0], b.p[0]);
+#pragma unroll
+  for (int i = 1; i < N / 2; ++i) s = __ffma2_rn(a.p[i], b.p[i], s);
+  return s.x + s.y;
 }
 
-// VEC consecutive values of one lane, in memory.
-template <typename T, int VEC> struct alignas(sizeof(T) * VEC) LaneVec { T e[VEC]; };
+// VEC consecutive values of one lane, in memory.  Streams are read and written once: `load` and
+// `store` mark their lines first to leave the L2.
+template <typename T, int VEC> struct alignas(sizeof(T) * VEC) LaneVec {
+  T e[VEC];
+  static constexpr int BYTES = sizeof(T) * VEC;
+  __device__ __forceinline__ void load(const T *p) {
+    if constexpr (BYTES == 16) *reinterpret_cast<uint4 *>(this) = __ldcs(reinterpret_cast<const uint4 *>(p));
+    else if constexpr (BYTES == 8) *reinterpret_cast<uint2 *>(this) = __ldcs(reinterpret_cast<const uint2 *>(p));
+    else if constexpr (BYTES == 4) *reinterpret_cast<uint32_t *>(this) = __ldcs(reinterpret_cast<const uint32_t *>(p));
+    else if constexpr (BYTES == 2) *reinterpret_cast<uint16_t *>(this) = __ldcs(reinterpret_cast<const uint16_t *>(p));
+    else *reinterpret_cast<uint8_t *>(this) = __ldcs(reinterpret_cast<const uint8_t *>(p));
+  }
+  // The same through the L1 as usual.
+  __device__ __forceinline__ void load_cached(const T *p) { *this = *reinterpret_cast<const LaneVec *>(p); }
+  __device__ __forceinline__ void store(T *p) const {
+    if constexpr (BYTES == 16) __stcs(reinterpret_cast<uint4 *>(p), *reinterpret_cast<const uint4 *>(this));
+    else if constexpr (BYTES == 8) __stcs(reinterpret_cast<uint2 *>(p), *reinterpret_cast<const uint2 *>(this));
+    else if constexpr (BYTES == 4) __stcs(reinterpret_cast<uint32_t *>(p), *reinterpret_cast<const uint32_t *>(this));
+    else if constexpr (BYTES == 2) __stcs(reinterpret_cast<uint16_t *>(p), *reinterpret_cast<const uint16_t *>(this));
+    else __stcs(reinterpret_cast<uint8_t *>(p), *reinterpret_cast<const uint8_t *>(this));
+  }
+};
 
-template <int VEC>
-__device__ __forceinline__ void widen(const LaneVec<float, VEC> &r, float (&f)[VEC]) {
+// Values AT .. AT + VEC - 1 of `f` from a lane's vector; codes are multiplied by their group's unit.
+template <int AT, int VEC, int N>
+__device__ __forceinline__ void widen(const LaneVec<float, VEC> &r, Pairs<N> &f) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) f[i] = r.e[i];
+  for (int i = 0; i < VEC; ++i) f.set(AT + i, r.e[i]);
 }
-template <int VEC>
-__device__ __forceinline__ void widen(const LaneVec<__nv_bfloat16, VEC> &r, float (&f)[VEC]) {
+template <int AT, int VEC, int N>
+__device__ __forceinline__ void widen(const LaneVec<__nv_bfloat16, VEC> &r, Pairs<N> &f) {
   if constexpr (VEC % 2 == 0) {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(&r);
 #pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) {  // a bf16 is the top half of the fp32 of the same value
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < VEC / 2; ++i)  // a bf16 is the top half of the fp32 of the same value
+      f.p[AT / 2 + i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  } else {
+    f.set(AT, __bfloat162float(r.e[0]));
+  }
+}
+// Each byte of the codes, offset by 128, becomes the low mantissa byte of 2^23 + 128 + code; the
+// difference and the product are exact.
+template <int AT, int VEC, int N>
+__device__ __forceinline__ void widen(const LaneVec<int8_t, VEC> &r, float unit, Pairs<N> &f) {
+  if constexpr (VEC % 4 == 0) {
+#pragma unroll
+    for (int k = 0; k < VEC / 4; ++k) {
+      const uint32_t o = reinterpret_cast<const uint32_t *>(&r)[k] ^ 0x80808080u;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 v = make_float2(__uint_as_float(__byte_perm(o, 0x4b000000u, 0x7440 + 2 * i)),
+                                     __uint_as_float(__byte_perm(o, 0x4b000000u, 0x7441 + 2 * i)));
+        f.p[AT / 2 + 2 * k + i] = __fmul2_rn(__fadd2_rn(v, splat(-8388736.f)), splat(unit));
+      }
     }
   } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = __bfloat162float(r.e[i]);
+    f.set(AT, (float)r.e[0] * unit);
   }
 }
-template <int VEC>
-__device__ __forceinline__ void widen(const LaneVec<int8_t, VEC> &r, float unit, float (&f)[VEC]) {
-  if constexpr (VEC % 4 == 0) {
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(&r);
+template <int AT, int VEC, int N>
+__device__ __forceinline__ void narrow(const Pairs<N> &f, LaneVec<float, VEC> &r) {
 #pragma unroll
-    for (int i = 0; i < VEC / 4; ++i) act8_value4(w[i], unit, f + 4 * i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = (float)r.e[i] * unit;
-  }
+  for (int i = 0; i < VEC; ++i) r.e[i] = f.get(AT + i);
 }
-template <int VEC>
-__device__ __forceinline__ void narrow(const float (&f)[VEC], LaneVec<float, VEC> &r) {
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) r.e[i] = f[i];
-}
-template <int VEC>
-__device__ __forceinline__ void narrow(const float (&f)[VEC], LaneVec<__nv_bfloat16, VEC> &r) {
+template <int AT, int VEC, int N>
+__device__ __forceinline__ void narrow(const Pairs<N> &f, LaneVec<__nv_bfloat16, VEC> &r) {
   if constexpr (VEC % 2 == 0) {
 #pragma unroll
-    for (int i = 0; i < VEC / 2; ++i)
-      reinterpret_cast<__nv_bfloat162 *>(&r)[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    for (int i = 0; i < VEC / 2; ++i) reinterpret_cast<__nv_bfloat162 *>(&r)[i] = __float22bfloat162_rn(f.p[AT / 2 + i]);
   } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) r.e[i] = __float2bfloat16_rn(f[i]);
+    r.e[0] = __float2bfloat16_rn(f.get(AT));
   }
 }
 
-// VEC consecutive fp32 values, 16 bytes at a time where VEC allows (p then on a 16-byte boundary).
+// The largest |x| bit pattern of a lane's vector.
 template <int VEC>
-__device__ __forceinline__ void load_f32(const float *p, float (&f)[VEC]) {
-  if constexpr (VEC % 4 == 0) {
+__device__ __forceinline__ uint32_t amax_bits(const LaneVec<float, VEC> &r) {
+  uint32_t m = __float_as_uint(r.e[0]) & 0x7fffffffu;
 #pragma unroll
-    for (int i = 0; i < VEC; i += 4) {
-      const float4 q = *reinterpret_cast<const float4 *>(p + i);
-      f[i] = q.x;
-      f[i + 1] = q.y;
-      f[i + 2] = q.z;
-      f[i + 3] = q.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = p[i];
-  }
+  for (int i = 1; i < VEC; ++i) m = max(m, __float_as_uint(r.e[i]) & 0x7fffffffu);
+  return m;
 }
 template <int VEC>
-__device__ __forceinline__ void store_f32(const float (&f)[VEC], float *p) {
-  if constexpr (VEC % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < VEC; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+__device__ __forceinline__ uint32_t amax_bits(const LaneVec<__nv_bfloat16, VEC> &r) {
+  if constexpr (VEC % 2 == 0) {  // two 15-bit patterns to a word
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(&r);
+    static_assert(VEC == 8, "four words");
+    uint32_t m = __vimax3_s16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu, w[2] & 0x7fff7fffu);
+    m = __vimax3_s16x2(m, m, w[3] & 0x7fff7fffu);
+    return max(m & 0xffff0000u, m << 16);
   } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) p[i] = f[i];
+    return (uint32_t)(__bfloat16_as_ushort(r.e[0]) & 0x7fffu) << 16;
   }
 }
 
-// The codes of a lane's VEC values and their group's scale byte; the 32 / VEC lanes that hold a
-// group are consecutive and aligned, and the whole warp calls this together (values past a row's
-// end are passed as 0).
-template <int VEC>
-__device__ __forceinline__ LaneVec<int8_t, VEC> act8_encode(const float (&x)[VEC], uint32_t &scale) {
+// The codes of a lane's vector r (`x` holds its values at AT onwards) and their group's scale byte;
+// the 32 / VEC lanes that hold a group are consecutive and aligned, and the whole warp calls this
+// together, a lane past its row's end with inside == false.  Adding 1.5 * 2^23 to x / scale leaves its
+// integer part in the last mantissa bits, rounded once by the fused multiply-add, ties to even.
+template <int AT, typename T, int VEC, int N>
+__device__ __forceinline__ LaneVec<int8_t, VEC> act8_encode(const LaneVec<T, VEC> &r, const Pairs<N> &x, bool inside,
+                                                            uint32_t &scale) {
   constexpr uint32_t TOP = 0x7f7e0000u;  // 127 * 2^121
-  uint32_t amax = 0;
-  float f[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    f[i] = x[i];
-    amax = max(amax, __float_as_uint(f[i]) & 0x7fffffffu);
-  }
+  uint32_t amax = inside ? amax_bits(r) : 0;
 #pragma unroll
   for (int m = 1; m < ACT_GROUP / VEC; m <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-  if (amax > TOP && amax < 0x7f800000u) {
-    amax = TOP;
+  float2 v[(VEC + 1) / 2];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = fminf(fmaxf(f[i], -__uint_as_float(TOP)), __uint_as_float(TOP));
+  for (int i = 0; i < (VEC + 1) / 2; ++i) v[i] = VEC == 1 ? make_float2(x.get(AT), 0.f) : x.p[AT / 2 + i];
+  if (amax > TOP && amax < 0x7f800000u) {  // hardly ever
+    const float t = __uint_as_float(TOP);
+#pragma unroll
+    for (int i = 0; i < (VEC + 1) / 2; ++i)
+      v[i] = make_float2(fminf(fmaxf(v[i].x, -t), t), fminf(fmaxf(v[i].y, -t), t));
+    amax = TOP;
   }
   scale = act8_scale(amax);
-  const float inv = act8_inverse(scale);
+  const float2 inv = splat(act8_inverse(scale));
+  uint32_t q[VEC + 1];
+#pragma unroll
+  for (int i = 0; i < (VEC + 1) / 2; ++i) {
+    const float2 c = __ffma2_rn(v[i], inv, splat(12582912.f));
+    q[2 * i] = __float_as_uint(c.x);
+    q[2 * i + 1] = __float_as_uint(c.y);
+  }
   LaneVec<int8_t, VEC> c;
   if constexpr (VEC % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < VEC / 4; ++i)
-      reinterpret_cast<uint32_t *>(&c)[i] = scale == 255u ? 0u : act8_code4(f + 4 * i, inv);
+    for (int i = 0; i < VEC / 4; ++i) {
+      const uint32_t lo = __byte_perm(q[4 * i], q[4 * i + 1], 0x0040), hi = __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040);
+      reinterpret_cast<uint32_t *>(&c)[i] = scale == 255u ? 0u : __byte_perm(lo, hi, 0x5410);
+    }
   } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) c.e[i] = scale == 255u ? 0 : (int8_t)act8_round(f[i], inv);
+    c.e[0] = scale == 255u ? 0 : (int8_t)q[0];
   }
   return c;
+}
+
+// N fp32 values that every row reads (weights), VEC at a time.
+template <int AT, int VEC, int N>
+__device__ __forceinline__ void load_f32(const float *p, Pairs<N> &f) {
+  if constexpr (VEC % 4 == 0) {  // p on a 16-byte boundary
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4) {
+      const float4 q = *reinterpret_cast<const float4 *>(p + i);
+      f.p[(AT + i) / 2] = make_float2(q.x, q.y);
+      f.p[(AT + i) / 2 + 1] = make_float2(q.z, q.w);
+    }
+  } else {
+    f.set(AT, p[0]);
+  }
+}
+template <int AT, int VEC, int N>
+__device__ __forceinline__ void store_f32(const Pairs<N> &f, float *p) {
+  if constexpr (VEC % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4)
+      *reinterpret_cast<float4 *>(p + i) = make_float4(f.p[(AT + i) / 2].x, f.p[(AT + i) / 2].y, f.p[(AT + i) / 2 + 1].x,
+                                                       f.p[(AT + i) / 2 + 1].y);
+  } else {
+    p[0] = f.get(AT);
+  }
 }
 
 // Sums of `parts` rows of `ncols` fp32 partial results, column by column in a fixed order, into up to
@@ -168,5 +228,9 @@ struct ColSumArgs {
   int end[3];     // first column past each output
 };
 cudaError_t launch_colsum(const ColSumArgs &a, cudaStream_t stream);
+
+// Raises a kernel's limit of dynamic shared memory to `bytes`, always the same for a kernel, on the
+// current device; `devices` remembers where that is done (one bit per device).
+cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> &devices);
 
 }  // namespace gdn2

@@ -4,13 +4,15 @@
 // gradients need of the forward is formed anew, in fp32.
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "act8.cuh"
 
 namespace gdn2 {
 namespace {
 
-constexpr int CE = 8;  // channels per lane
+constexpr int CE = 8;  // channels per lane of the pointwise passes
+constexpr int CC = 4;  // channels per lane of the convolution paths
 constexpr float L2_EPS = 1e-6f, RMS_EPS = 1e-5f;
 
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -23,41 +25,63 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// sigmoid(x) = 1 / (1 + 2^(-x log2 e)); 0 and 1 at the far ends.
-__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.f + ex2_approx(-1.4426950408889634f * x)); }
+// sigmoid(x) = 1 / (1 + 2^(-x log2 e)) of a pair; 0 and 1 at the far ends.
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  const float2 m = __fmul2_rn(x, splat(-1.4426950408889634f));
+  const float2 den = __fadd2_rn(make_float2(ex2_approx(m.x), ex2_approx(m.y)), splat(1.f));
+  return make_float2(rcp_approx(den.x), rcp_approx(den.y));
+}
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 1 - s of a pair.
+__device__ __forceinline__ float2 one_minus2(float2 s) { return __ffma2_rn(s, splat(-1.f), splat(1.f)); }
 
-// The CE channels of a lane, as loaded: 16-byte words in the element type, one 8-byte word of codes.
-template <typename S> struct Lane {
-  static constexpr int VEC = sizeof(S) == 4 ? 4 : CE;
-  LaneVec<S, VEC> v[CE / VEC];
+// N channels of a lane, as loaded: words of 16 bytes at most.
+template <typename S, int N> struct Lane {
+  static constexpr int VEC = sizeof(S) == 4 ? 4 : N, WORDS = N / VEC;
+  LaneVec<S, VEC> v[WORDS];
   __device__ __forceinline__ void load(const S *p) {
 #pragma unroll
-    for (int i = 0; i < CE / VEC; ++i) v[i] = reinterpret_cast<const LaneVec<S, VEC> *>(p)[i];
+    for (int i = 0; i < WORDS; ++i) v[i].load(p + i * VEC);
+  }
+  __device__ __forceinline__ void load_cached(const S *p) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) v[i].load_cached(p + i * VEC);
   }
   __device__ __forceinline__ void store(S *p) const {
 #pragma unroll
-    for (int i = 0; i < CE / VEC; ++i) reinterpret_cast<LaneVec<S, VEC> *>(p)[i] = v[i];
+    for (int i = 0; i < WORDS; ++i) v[i].store(p + i * VEC);
   }
-  __device__ __forceinline__ void get(float (&f)[CE], float unit) const {
-#pragma unroll
-    for (int i = 0; i < CE / VEC; ++i) {
-      float t[VEC];
-      if constexpr (sizeof(S) == 1) widen(v[i], unit, t);
-      else widen(v[i], t);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) f[i * VEC + k] = t[k];
+  __device__ __forceinline__ void get(Pairs<N> &f, float unit) const {
+    if constexpr (sizeof(S) == 1) {
+      widen<0, VEC>(v[0], unit, f);
+    } else {
+      widen<0, VEC>(v[0], f);
+      if constexpr (WORDS == 2) widen<VEC, VEC>(v[1], f);
     }
   }
-  __device__ __forceinline__ void put(const float (&f)[CE]) {
-#pragma unroll
-    for (int i = 0; i < CE / VEC; ++i) {
-      float t[VEC];
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) t[k] = f[i * VEC + k];
-      narrow(t, v[i]);
-    }
+  __device__ __forceinline__ void put(const Pairs<N> &f) {
+    narrow<0, VEC>(f, v[0]);
+    if constexpr (WORDS == 2) narrow<VEC, VEC>(f, v[1]);
   }
 };
+
+// d <- sign d p (1 - p), p = sigmoid(x): p (1 - p) = e / (1 + e)^2 with e = 2^-(|x| log2 e), which neither
+// cancels nor overflows, and 1 + e <= 2 lets one reciprocal serve a pair.
+template <int N> __device__ __forceinline__ void gate_bwd(const Pairs<N> &x, Pairs<N> &d, float sign) {
+#pragma unroll
+  for (int c = 0; c < N / 2; ++c) {
+    const float2 e = make_float2(ex2_approx(-1.4426950408889634f * fabsf(x.p[c].x)),
+                                 ex2_approx(-1.4426950408889634f * fabsf(x.p[c].y)));
+    const float2 den = __fadd2_rn(e, splat(1.f));
+    const float r = rcp_approx(den.x * den.y);
+    const float2 p = __fmul2_rn(splat(r), make_float2(den.y, den.x));
+    d.p[c] = __fmul2_rn(__fmul2_rn(d.p[c], e), __fmul2_rn(p, __fmul2_rn(p, splat(sign))));
+  }
+}
 
 // Sum over the G lanes of a row (G a power of two, the lanes aligned within their warp).
 template <int G>
@@ -67,6 +91,13 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
+// Asynchronous copy of BYTES (4, 8 or 16) from global to shared memory.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void *smem, const void *gmem) {
+  const uint32_t s = (uint32_t)__cvta_generic_to_shared(smem);
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(gmem) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(s), "l"(gmem), "n"(BYTES) : "memory");
+}
 // ---------------------------------------------------------------------------------------- epilogue
 //
 // y = oh g s with oh = o r, r = 1 / sqrt(mean o^2 + eps), s = z sigmoid(z).  With e = dy g s:
@@ -74,98 +105,99 @@ __device__ __forceinline__ float row_sum(float x) {
 // dy oh s.  A row of d_v values is held by G = d_v / 8 lanes, 8 per lane; groups of lanes take rows in
 // turn and keep their dg in registers.  HBM-bound: each value is read once and written once.
 
-constexpr int ER = 2;  // rows whose loads a lane has in flight
+// Blocks per SM: what 128 (fp32), 80 (bf16) or 64 registers (bf16 from 8 bits: its loads are half as wide,
+// and a fourth block pays for a few spills: 162 us instead of 171 on 12345 x 32 x 256) allow.
+constexpr int EPI_THREADS = 256;
+template <typename T, typename S> __host__ __device__ constexpr int epi_blocks() {
+  return sizeof(T) == 4 ? 2 : sizeof(S) == 1 ? 4 : 3;
+}
 
 template <typename T, typename S, int DV>
-__global__ void __launch_bounds__(256) epilogue_bwd_kernel(const EpilogueBwdArgs a, float *parts) {
-  constexpr int G = DV / CE, GROUPS = 256 / G;
+__global__ void __launch_bounds__(EPI_THREADS, epi_blocks<T, S>()) epilogue_bwd_kernel(const EpilogueBwdArgs a, float *parts) {
+  constexpr int G = DV / CE, GROUPS = EPI_THREADS / G, TILE = EPI_THREADS * CE;  // whole rows
   constexpr bool Q = sizeof(S) == 1;
   __shared__ float red[GROUPS][DV];
   const int grp = threadIdx.x / G, c = (threadIdx.x % G) * CE;
-  float g[CE], dg[CE];
+  const unsigned off = threadIdx.x * CE;  // a lane's place in every tile
+  Pairs<CE> g, dg;
+  fill(dg, 0.f);
 #pragma unroll
-  for (int i = 0; i < CE; ++i) {
-    g[i] = a.g[c + i];
-    dg[i] = 0.f;
-  }
-  const long long step = (long long)gridDim.x * GROUPS * ER;
-  for (long long row0 = (long long)blockIdx.x * GROUPS * ER; row0 < a.rows; row0 += step) {
-    Lane<S> ro[ER], rz[ER];
-    Lane<T> ry[ER];
-    float uo[ER], uz[ER];
-#pragma unroll
-    for (int u = 0; u < ER; ++u) {
-      const long long row = row0 + u * GROUPS + grp;
-      if (row < a.rows) {
-        const size_t at = (size_t)row * DV + c;
-        ro[u].load(static_cast<const S *>(a.o) + at);
-        rz[u].load(static_cast<const S *>(a.z) + at);
-        ry[u].load(static_cast<const T *>(a.dy) + at);
-        if (Q) {
-          uo[u] = act8_unit(a.o_scales[at / ACT_GROUP]);
-          uz[u] = act8_unit(a.z_scales[at / ACT_GROUP]);
-        }
-      }
+  for (int i = 0; i < CE; ++i) g.set(i, a.g[c + i]);
+  const long long total = a.rows * DV, step = (long long)gridDim.x * TILE;
+  Lane<S, CE> ro, rz;
+  Lane<T, CE> ry;
+  uint8_t so = 0, sz = 0;
+  auto inside = [&](long long base) { return off < (unsigned)min(total - base, (long long)TILE); };
+  auto load = [&](long long base) {  // (marked to leave the L2 first, the loads cost 3 % here)
+    if (!inside(base)) return;
+    ro.load_cached(static_cast<const S *>(a.o) + base + off);
+    rz.load_cached(static_cast<const S *>(a.z) + base + off);
+    ry.load_cached(static_cast<const T *>(a.dy) + base + off);
+    if (Q) {
+      so = a.o_scales[base / ACT_GROUP + off / ACT_GROUP];
+      sz = a.z_scales[base / ACT_GROUP + off / ACT_GROUP];
     }
+  };
+  long long base = (long long)blockIdx.x * TILE;
+  load(base);
+  for (; base < total; base += step) {
+    const bool live = inside(base);
+    Pairs<CE> o, z, e;
+    if (live) {
+      ro.get(o, Q ? act8_unit(so) : 0.f);
+      rz.get(z, Q ? act8_unit(sz) : 0.f);
+      ry.get(e, 0.f);
+    } else {  // the sums shuffle whole warps
+      fill(o, 0.f);
+      fill(z, 0.f);
+      fill(e, 0.f);
+    }
+    if (base + step < total) load(base + step);
+    const float r = rsqrt_approx(row_sum<G>(dot(o, o)) * (1.f / DV) + RMS_EPS);
 #pragma unroll
-    for (int u = 0; u < ER; ++u) {
-      const long long row = row0 + u * GROUPS + grp;
-      const bool live = row < a.rows;
-      float o[CE], z[CE], e[CE], ss = 0.f, eo = 0.f;
-      if (live) {
-        ro[u].get(o, uo[u]);
-        rz[u].get(z, uz[u]);
-        ry[u].get(e, 0.f);
+    for (int i = 0; i < CE / 2; ++i) {
+      const float2 sg = sigmoid2(z.p[i]), s = __fmul2_rn(z.p[i], sg);
+      o.p[i] = __fmul2_rn(o.p[i], splat(r));  // oh
+      const float2 yo = __fmul2_rn(e.p[i], o.p[i]), yg = __fmul2_rn(e.p[i], g.p[i]);
+      dg.p[i] = __ffma2_rn(yo, s, dg.p[i]);
+      z.p[i] = __fmul2_rn(__fmul2_rn(yo, g.p[i]), __ffma2_rn(s, one_minus2(sg), sg));  // dz
+      e.p[i] = __fmul2_rn(yg, s);
+    }
+    const float m = row_sum<G>(dot(e, o)) * (-1.f / DV);
+    if (live) {
 #pragma unroll
-        for (int i = 0; i < CE; ++i) ss = fmaf(o[i], o[i], ss);
-      }
-      ss = row_sum<G>(ss);
-      const float r = rsqrtf(ss * (1.f / DV) + RMS_EPS);
-      if (live) {
-#pragma unroll
-        for (int i = 0; i < CE; ++i) {
-          const float sg = sigmoid(z[i]), s = z[i] * sg, oh = o[i] * r, yo = e[i] * oh;
-          dg[i] = fmaf(yo, s, dg[i]);
-          z[i] = yo * g[i] * fmaf(s, 1.f - sg, sg);  // dz
-          e[i] *= g[i] * s;
-          eo = fmaf(e[i], oh, eo);
-          o[i] = oh;
-        }
-      }
-      eo = row_sum<G>(eo) * (1.f / DV);
-      if (live) {
-#pragma unroll
-        for (int i = 0; i < CE; ++i) e[i] = r * (e[i] - o[i] * eo);
-        const size_t at = (size_t)row * DV + c;
-        ry[u].put(e);
-        ry[u].store(static_cast<T *>(a.dout) + at);
-        ry[u].put(z);
-        ry[u].store(static_cast<T *>(a.dz) + at);
-      }
+      for (int i = 0; i < CE / 2; ++i) e.p[i] = __fmul2_rn(splat(r), __ffma2_rn(o.p[i], splat(m), e.p[i]));
+      Lane<T, CE> out;
+      out.put(e);
+      out.store(static_cast<T *>(a.dout) + base + off);
+      out.put(z);
+      out.store(static_cast<T *>(a.dz) + base + off);
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < CE; ++i) red[grp][c + i] = dg[i];
+  for (int i = 0; i < CE; ++i) red[grp][c + i] = dg.get(i);
   __syncthreads();
-  for (int k = threadIdx.x; k < DV; k += 256) {
+  for (int k = threadIdx.x; k < DV; k += EPI_THREADS) {
     float s = 0.f;
+#pragma unroll 8
     for (int w = 0; w < GROUPS; ++w) s += red[w][k];
     parts[(size_t)blockIdx.x * DV + k] = s;
   }
 }
 
-int epilogue_blocks(long long rows, int dv) {
-  const long long per = (long long)256 / (dv / CE) * ER;
-  return (int)std::max<long long>(1, std::min<long long>((rows + per - 1) / per, (long long)sm_count() * 4));
+int epilogue_blocks(long long rows, int dv, int per_sm) {
+  const long long per = EPI_THREADS / (dv / CE), most = (long long)sm_count() * per_sm;
+  return (int)std::max(1ll, std::min((rows + per - 1) / per, most));
 }
 
 template <typename T, typename S>
 cudaError_t epilogue_t(const EpilogueBwdArgs &a, float *parts, cudaStream_t stream) {
-  const int blocks = epilogue_blocks(a.rows, a.dv);
+  const int blocks = epilogue_blocks(a.rows, a.dv, epi_blocks<T, S>());
   note_launch();
-  if (a.dv == 64) epilogue_bwd_kernel<T, S, 64><<<blocks, 256, 0, stream>>>(a, parts);
-  else if (a.dv == 128) epilogue_bwd_kernel<T, S, 128><<<blocks, 256, 0, stream>>>(a, parts);
-  else epilogue_bwd_kernel<T, S, 256><<<blocks, 256, 0, stream>>>(a, parts);
+  if (a.dv == 64) epilogue_bwd_kernel<T, S, 64><<<blocks, EPI_THREADS, 0, stream>>>(a, parts);
+  else if (a.dv == 128) epilogue_bwd_kernel<T, S, 128><<<blocks, EPI_THREADS, 0, stream>>>(a, parts);
+  else epilogue_bwd_kernel<T, S, 256><<<blocks, EPI_THREADS, 0, stream>>>(a, parts);
   const cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   return launch_colsum({parts, blocks, a.dv, {a.dg, nullptr, nullptr}, {a.dv, a.dv, a.dv}}, stream);
@@ -177,35 +209,31 @@ cudaError_t epilogue_t(const EpilogueBwdArgs &a, float *parts, cudaStream_t stre
 // sequence), s = y sigmoid(y), and for q and k the unit row n s, n = 1 / sqrt(sum s^2 + eps).
 // ds = n d - n^3 s (s . d) (v: ds = d); dy = ds sigmoid(y) (1 + y (1 - sigmoid(y)));
 // dx_t = sum_j w_j dy_{t+j}, dw_j = sum_t dy_t x_{t-j}, inside the sequence both.
+// Gates: alpha = sigmoid(-x), b and w = sigmoid(x): dx = +- d p (1 - p), p = sigmoid(x).
 //
-// A group of d / 8 lanes holds one (token, head) row, 8 channels per lane, and walks a run of R tokens
-// of one head forwards.  dx_t is complete once dy_{t+K-1} is known, so three unfinished dx and the
+// A block holds up to 512 neighbouring channels of one path, 4 per lane, so that d / 4 lanes hold one
+// (token, head) row, and walks a run of R tokens forwards.  dx_t is complete once dy_{t+K-1} is known, so three unfinished dx and the
 // three previous x stay in registers beside the taps and their gradients; each run walks K - 1 tokens
-// further than it writes.  The taps' gradients of a run leave as one row of partial sums.
+// further than it writes.  The taps' gradients of a run leave as one row of partial sums.  Every lane
+// also takes the gate of its path's width (alpha with q, b with k, w with v) at the same offsets: the
+// gates are pure traffic, the convolutions mostly arithmetic, and so the two overlap.
 
-constexpr int CT = 128;  // threads of a block
-constexpr int CS = 3;    // load batches in a lane's ring (two in flight while one is used)
+constexpr int CT = 128;           // threads of a block, at most
+constexpr int CONV_BLOCKS = 4;    // blocks of that many threads per SM
+constexpr int GATE_TILES = 32;    // blocks of the gates per SM, at most
+constexpr int CS = 2;             // load batches in a lane's ring (one is used, the other in flight)
 
-struct ConvBwdPath {
-  const void *x;
-  const uint8_t *scales;
+struct PathBwd {  // a convolution path and the gate that goes with it
+  const void *x, *d, *gx, *gd;
+  void *dx, *gdx;
+  const uint8_t *scales, *gscales;
   const float *W;
-  const void *d;
-  void *dx;
   int dim, l2, col;  // col: the path's first column in a row of partial sums
-  long long blocks;  // of its runs
-};
-struct GateBwdPath {
-  const void *x;
-  const uint8_t *scales;
-  const void *d;
-  void *dx;
-  int dim;
-  float sign;
+  float sign;        // of the gate's derivative
+  int blocks;        // of one run's channels
 };
 struct ConvBwdArgs {
-  ConvBwdPath conv[3];
-  GateBwdPath gate[3];
+  PathBwd path[3];
   const int32_t *cu;
   float *parts;  // [runs][ncols]
   int ncols, N, T, H, K, R;
@@ -213,109 +241,91 @@ struct ConvBwdArgs {
   int gate_blocks;
 };
 
-__device__ __forceinline__ void cp_async(void *smem, const void *gmem, int bytes, int src) {
-  const uint32_t s = (uint32_t)__cvta_generic_to_shared(smem);
-  if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(gmem) : "memory");
-  else if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(s), "l"(gmem) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(s), "l"(gmem), "r"(src) : "memory");
-}
-
-// One batch of a block's ring, [token][word][thread] for each of its arrays.
+// A lane's ring: per batch and token x and d, each [thread].
 template <typename T, typename S> struct Ring {
-  static constexpr int CU = 16 / (int)sizeof(T) / 2;  // tokens per batch: 4 (bf16), 2 (fp32)
-  static constexpr bool Q = sizeof(S) == 1;
-  static constexpr int XW = Q ? 1 : CE * (int)sizeof(S) / 16, DW = CE * (int)sizeof(T) / 16;
-  static constexpr int XB = Q ? 8 : 16;  // bytes of a word of x
-  static constexpr int X = 0, D = X + CU * XW * XB * CT, SC = D + CU * DW * 16 * CT;
-  static constexpr int BYTES = SC + (Q ? CU * 4 * CT : 0);
+  static constexpr int CU = 4;  // tokens per batch
+  static constexpr int XB = CC * (int)sizeof(S), DB = CC * (int)sizeof(T);
+  static constexpr int X = 0, D = X + XB * CT, TOKEN = D + DB * CT, BATCH = TOKEN * CU;
 };
 
-// The gates: alpha = sigmoid(-x), b and w = sigmoid(x); each has dx = +- d p (1 - p), p = sigmoid(x),
-// formed as 2^-|..| / (1 + 2^-|..|)^2, which neither cancels nor overflows.
+// Vectors that a lane of the gates has in flight: 128 bytes of each input.
+template <typename T> __host__ __device__ constexpr int gate_unroll() { return sizeof(T) == 2 ? 8 : 4; }
+// The gates: tiles of U vectors per lane over the three paths end to end, taken in turn by the blocks.
 template <typename T, typename S>
-__device__ void gate_bwd(const ConvBwdArgs &a, int block) {
+__device__ __forceinline__ void gates_bwd(const ConvBwdArgs &a, int block) {
   constexpr bool Q = sizeof(S) == 1;
-  constexpr int U = 2;
+  constexpr int U = gate_unroll<T>();
   const long long live = a.cu ? min((long long)a.cu[a.N], a.tokens) : a.tokens;
-#pragma unroll 1
-  for (int k = 0; k < 3; ++k) {
-    const GateBwdPath P = k == 0 ? a.gate[0] : k == 1 ? a.gate[1] : a.gate[2];
-    const long long nvec = live * a.H * (P.dim / CE);
-    for (long long b = (long long)block * (CT * U); b < nvec; b += (long long)a.gate_blocks * (CT * U)) {
-      Lane<S> rx[U];
-      Lane<T> rd[U];
-      float unit[U];
+  const int span = blockDim.x * U;
+  const long long nk = max(0ll, live) * a.H * (a.path[0].dim / CE), nv = max(0ll, live) * a.H * (a.path[2].dim / CE);
+  const long long tk = (nk + span - 1) / span, tiles = 2 * tk + (nv + span - 1) / span;
+  for (long long t = block; t < tiles; t += a.gate_blocks) {
+    const int k = t < tk ? 0 : t < 2 * tk ? 1 : 2;
+    const PathBwd &P = a.path[k];
+    const long long b = (t - k * tk) * span;
+    const S *x = static_cast<const S *>(P.gx) + b * CE;
+    const T *d = static_cast<const T *>(P.gd) + b * CE;
+    T *dx = static_cast<T *>(P.gdx) + b * CE;
+    const int n = (int)min((k < 2 ? nk : nv) - b, (long long)span);
+    Lane<S, CE> rx[U];
+    Lane<T, CE> rd[U];
+    uint8_t sc[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const long long i = b + u * CT + threadIdx.x;
-        if (i < nvec) {
-          rx[u].load(static_cast<const S *>(P.x) + i * CE);
-          rd[u].load(static_cast<const T *>(P.d) + i * CE);
-          if (Q) unit[u] = act8_unit(P.scales[i / (ACT_GROUP / CE)]);
-        }
+    for (int u = 0; u < U; ++u) {
+      const int i = u * blockDim.x + threadIdx.x;
+      if (i < n) {
+        rx[u].load(x + i * CE);
+        rd[u].load(d + i * CE);
+        if (Q) sc[u] = P.gscales[b / (ACT_GROUP / CE) + i / (ACT_GROUP / CE)];
       }
+    }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const long long i = b + u * CT + threadIdx.x;
-        if (i < nvec) {
-          float x[CE], d[CE];
-          rx[u].get(x, unit[u]);
-          rd[u].get(d, 0.f);
-#pragma unroll
-          for (int c = 0; c < CE; ++c) {
-            const float e = ex2_approx(-1.4426950408889634f * fabsf(x[c])), p = rcp_approx(1.f + e);
-            d[c] *= P.sign * e * p * p;
-          }
-          rd[u].put(d);
-          rd[u].store(static_cast<T *>(P.dx) + i * CE);
-        }
+    for (int u = 0; u < U; ++u) {
+      const int i = u * blockDim.x + threadIdx.x;
+      if (i < n) {
+        Pairs<CE> xf, df;
+        rx[u].get(xf, Q ? act8_unit(sc[u]) : 0.f);
+        rd[u].get(df, 0.f);
+        gate_bwd(xf, df, P.sign);
+        rd[u].put(df);
+        rd[u].store(dx + i * CE);
       }
     }
   }
 }
 
-template <typename T, typename S>
-__global__ void __launch_bounds__(CT, 3) prologue_bwd_kernel(const ConvBwdArgs a) {
+// One block's run of one path; G: lanes of a row whose norm is taken, 0 for a path without one.
+template <typename T, typename S, int G>
+__device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P, int blk, long long run, uint8_t *ring) {
   using RB = Ring<T, S>;
   constexpr int CU = RB::CU;
-  constexpr bool Q = RB::Q;
-  extern __shared__ __align__(16) uint8_t ring[];
-  long long blk = blockIdx.x;
-  int path = 0;
-  while (path < 3 && blk >= a.conv[path].blocks) blk -= a.conv[path++].blocks;
-  if (path == 3) {
-    gate_bwd<T, S>(a, (int)blk);
-    return;
-  }
-  const ConvBwdPath P = path == 0 ? a.conv[0] : path == 1 ? a.conv[1] : a.conv[2];
-  const int G = P.dim / CE, K = a.K;
-  const long long gid = (blk * CT + threadIdx.x) / G;
-  if (gid >= a.runs * a.H) return;  // whole groups leave together
-  const int lane = threadIdx.x & 31, gl = lane & (G - 1);
-  const unsigned gmask = G == 32 ? 0xffffffffu : ((1u << G) - 1u) << (lane & ~(G - 1));
-  const int h = (int)(gid % a.H);
-  const long long run = gid / a.H, t0 = run * a.R;
+  constexpr bool Q = sizeof(S) == 1;
+  const long long t0 = run * a.R;
+  const int K = a.K;
+  const unsigned stride = (unsigned)a.H * P.dim;  // elements between tokens; a run's offsets fit 32 bits
+  const unsigned ch = (blk * blockDim.x + threadIdx.x) * CC;
+  if (ch >= stride) return;  // whole groups leave together
+  const int lane = threadIdx.x & 31;
+  const unsigned gmask = G == 0 || G == 32 ? 0xffffffffu : ((1u << (G & 31)) - 1u) << (lane & ~(G - 1));
   const long long live = a.cu ? min((long long)a.cu[a.N], a.tokens) : a.tokens;  // rows behind it are not touched
-  const size_t stride = (size_t)a.H * P.dim, first = (size_t)t0 * stride + (size_t)h * P.dim + gl * CE;
-  const int ch = h * P.dim + gl * CE;
-  float *part = a.parts + (size_t)run * a.ncols + P.col + (size_t)ch * K;
+  const size_t at0 = (size_t)t0 * stride;
 
-  float w[4][CE], dw[4][CE];
+  Pairs<CC> w[4], dw[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < 4; ++j) {
+    fill(dw[j], 0.f);
 #pragma unroll
-    for (int i = 0; i < CE; ++i) {
-      w[j][i] = j < K ? P.W[(size_t)(ch + i) * K + K - 1 - j] : 0.f;
-      dw[j][i] = 0.f;
-    }
-  const int ntok = (int)max(0ll, min((long long)a.R, live - t0));      // tokens of the run
+    for (int i = 0; i < CC; ++i) w[j].set(i, j < K ? P.W[(size_t)(ch + i) * K + K - 1 - j] : 0.f);
+  }
+  const int ntok = (int)max(0ll, min((long long)a.R, live - t0));           // tokens of the run
   const int nload = (int)max(0ll, min((long long)a.R + K - 1, live - t0));  // and those its dx reach
   if (ntok > 0) {
-    // the sequence holding t0: its first token s0, and the next sequence's start nb (beyond: none)
+    // the sequence holding t0: its first token s0, and the next sequence's start nbr (beyond: none);
+    // both relative to t0, as all token indices below
     long long s0, nb;
     int n = 0;
     if (!a.cu) {
-      s0 = t0 - t0 % a.T;
+      s0 = -(t0 % a.T);
       nb = s0 + a.T;
     } else {
       int lo = 0, hi = a.N - 1;
@@ -324,143 +334,139 @@ __global__ void __launch_bounds__(CT, 3) prologue_bwd_kernel(const ConvBwdArgs a
         if (a.cu[mid] <= t0) lo = mid; else hi = mid - 1;
       }
       n = lo;
-      s0 = a.cu[n];
-      nb = a.cu[n + 1];
-      if (nb <= t0) nb = LLONG_MAX;
+      s0 = a.cu[n] - t0;
+      nb = a.cu[n + 1] - t0;
+      if (nb <= 0) nb = INT_MAX;
     }
-    const S *x = static_cast<const S *>(P.x);
-    const T *d = static_cast<const T *>(P.d) + first;
-    T *dx = static_cast<T *>(P.dx) + first;
-    float x1[CE], x2[CE], x3[CE], p1[CE], p2[CE], p3[CE];  // x_{t-j}; unfinished dx_{t-j}
-#pragma unroll
-    for (int i = 0; i < CE; ++i) x1[i] = x2[i] = x3[i] = p1[i] = p2[i] = p3[i] = 0.f;
-#pragma unroll
-    for (int j = 1; j <= 3; ++j)
-      if (t0 - j >= max(s0, 0ll)) {
-        const size_t at = first - (size_t)j * stride;
-        Lane<S> r;
-        r.load(x + at);
-        r.get(j == 1 ? x1 : (j == 2 ? x2 : x3), Q ? act8_unit(P.scales[at / ACT_GROUP]) : 0.f);
-      }
+    int nbr = (int)min(nb, (long long)INT_MAX);
+    Pairs<CC> x1, x2, x3, p1, p2, p3;  // x_{t-j}; unfinished dx_{t-j}
+    auto clear = [&] {
+      fill(x1, 0.f);
+      fill(x2, 0.f);
+      fill(x3, 0.f);
+      fill(p1, 0.f);
+      fill(p2, 0.f);
+      fill(p3, 0.f);
+    };
+    clear();
+    auto before = [&](int j, Pairs<CC> &f) {
+      if (-j < max(s0, -t0)) return;
+      const size_t at = at0 + ch - (size_t)j * stride;
+      Lane<S, CC> r;
+      r.load(static_cast<const S *>(P.x) + at);
+      r.get(f, Q ? act8_unit(P.scales[at / ACT_GROUP]) : 0.f);
+    };
+    before(1, x1);
+    before(2, x2);
+    before(3, x3);
+    const S *const x = static_cast<const S *>(P.x) + at0;
+    const T *const d = static_cast<const T *>(P.d) + at0;
+    T *const dx = static_cast<T *>(P.dx) + at0;
+    const uint8_t *const sc = P.scales + at0 / ACT_GROUP;
+    uint8_t ahead[CU];  // scale bytes of the batch in flight
     const int nbatch = (nload + CU - 1) / CU;
-    const size_t scale_end = (size_t)a.tokens * stride / ACT_GROUP;
     auto issue = [&](int bt) {  // copies of batch bt, committed as one group
-      uint8_t *slot = ring + (bt % CS) * RB::BYTES;
+      uint8_t *slot = ring + (bt % CS) * RB::BATCH;
 #pragma unroll
       for (int u = 0; u < CU; ++u) {
         const int i = bt * CU + u;
         if (i < nload) {
-          const size_t at = first + (size_t)i * stride;
-#pragma unroll
-          for (int v = 0; v < RB::XW; ++v)
-            cp_async(slot + RB::X + ((u * RB::XW + v) * CT + threadIdx.x) * RB::XB,
-                     reinterpret_cast<const uint8_t *>(x + at) + v * RB::XB, RB::XB, RB::XB);
-#pragma unroll
-          for (int v = 0; v < RB::DW; ++v)
-            cp_async(slot + RB::D + ((u * RB::DW + v) * CT + threadIdx.x) * 16,
-                     reinterpret_cast<const uint8_t *>(d + (size_t)i * stride) + v * 16, 16, 16);
-          if (Q) {  // the aligned word that holds the group's scale byte, up to the array's end
-            const size_t sa = at / ACT_GROUP & ~(size_t)3;
-            cp_async(slot + RB::SC + (u * CT + threadIdx.x) * 4, P.scales + sa, 4, (int)min((size_t)4, scale_end - sa));
-          }
+          const unsigned o = (unsigned)i * stride + ch;
+          uint8_t *to = slot + u * RB::TOKEN;
+          cp_async<RB::XB>(to + RB::X + threadIdx.x * RB::XB, x + o);
+          cp_async<RB::DB>(to + RB::D + threadIdx.x * RB::DB, d + o);
+          if (Q) ahead[u] = sc[o / ACT_GROUP];
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    int lo = 0;  // first token of the run in the current sequence (relative to t0, as all below)
-    int nbr = (int)min(nb - t0, (long long)INT_MAX);
-    auto put = [&](int i, const float (&f)[CE]) {
-      Lane<T> r;
-      r.put(f);
-      r.store(dx + (size_t)i * stride);
-    };
-    auto token = [&](int i, int u, const uint8_t *slot, bool checked) {
-      float xt[CE], y[CE], g[CE];
-      {
-        Lane<S> rx;
-        Lane<T> rd;
-        float unit = 0.f;
+    int lo = 0;  // first token of the run in the current sequence
+    auto token = [&](int i, const uint8_t *from, float unit, auto checked) {
+      constexpr bool CHECK = decltype(checked)::value;
+      const unsigned o = (unsigned)i * stride + ch;
+      Pairs<CC> xt, y, g, ds;
+      Lane<S, CC> rx;
+      Lane<T, CC> rd;
+      rx.v[0] = *reinterpret_cast<const LaneVec<S, CC> *>(from + RB::X + threadIdx.x * RB::XB);
+      rd.v[0] = *reinterpret_cast<const LaneVec<T, CC> *>(from + RB::D + threadIdx.x * RB::DB);
+      rx.get(xt, unit);
+      rd.get(g, 0.f);
 #pragma unroll
-        for (int v = 0; v < RB::XW; ++v)
-          rx.v[v] = *reinterpret_cast<const LaneVec<S, Lane<S>::VEC> *>(
-              slot + RB::X + ((u * RB::XW + v) * CT + threadIdx.x) * RB::XB);
-#pragma unroll
-        for (int v = 0; v < RB::DW; ++v)
-          rd.v[v] = *reinterpret_cast<const LaneVec<T, Lane<T>::VEC> *>(
-              slot + RB::D + ((u * RB::DW + v) * CT + threadIdx.x) * 16);
-        if (Q) {
-          const size_t sa = (first + (size_t)i * stride) / ACT_GROUP;
-          unit = act8_unit(slot[RB::SC + (u * CT + threadIdx.x) * 4 + (sa & 3)]);
-        }
-        rx.get(xt, unit);
-        rd.get(g, 0.f);
+      for (int c = 0; c < CC / 2; ++c) {
+        float2 v = __fmul2_rn(w[0].p[c], xt.p[c]);
+        v = __ffma2_rn(w[1].p[c], x1.p[c], v);
+        v = __ffma2_rn(w[2].p[c], x2.p[c], v);
+        v = __ffma2_rn(w[3].p[c], x3.p[c], v);
+        const float2 sg = sigmoid2(v);
+        y.p[c] = __fmul2_rn(v, sg);
+        ds.p[c] = __ffma2_rn(y.p[c], one_minus2(sg), sg);  // derivative of SiLU
       }
-      float ss = 0.f, sd = 0.f;
-      float ds[CE];  // derivative of SiLU at y
+      if constexpr (G > 0) {
+        // both sums in one pass: even lanes end with sum y^2, odd ones with sum y d
+        const float ss = dot(y, y), sd = dot(y, g);
+        const bool odd = lane & 1;
+        float s = (odd ? sd : ss) + __shfl_xor_sync(gmask, odd ? ss : sd, 1);
 #pragma unroll
-      for (int c = 0; c < CE; ++c) {
-        float v = w[0][c] * xt[c];
-        v = fmaf(w[1][c], x1[c], v);
-        v = fmaf(w[2][c], x2[c], v);
-        v = fmaf(w[3][c], x3[c], v);
-        const float sg = sigmoid(v);
-        y[c] = v * sg;
-        ds[c] = fmaf(y[c], 1.f - sg, sg);
-        ss = fmaf(y[c], y[c], ss);
-        sd = fmaf(y[c], g[c], sd);
-      }
-      if (P.l2) {
+        for (int m = 2; m < G; m <<= 1) s += __shfl_xor_sync(gmask, s, m);
+        const float other = __shfl_xor_sync(gmask, s, 1);
+        const float nrm = rsqrt_approx((odd ? other : s) + L2_EPS), k3 = -nrm * nrm * nrm * (odd ? s : other);
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1)
-          if (m < G) {
-            ss += __shfl_xor_sync(gmask, ss, m);
-            sd += __shfl_xor_sync(gmask, sd, m);
-          }
-        const float nrm = rsqrtf(ss + L2_EPS), k3 = nrm * nrm * nrm * sd;
-#pragma unroll
-        for (int c = 0; c < CE; ++c) g[c] = fmaf(-k3, y[c], nrm * g[c]);
+        for (int c = 0; c < CC / 2; ++c) g.p[c] = __ffma2_rn(splat(k3), y.p[c], __fmul2_rn(splat(nrm), g.p[c]));
       }
 #pragma unroll
-      for (int c = 0; c < CE; ++c) g[c] *= ds[c];  // dy
-      if (!checked || i < ntok) {
+      for (int c = 0; c < CC / 2; ++c) g.p[c] = __fmul2_rn(g.p[c], ds.p[c]);  // dy
+      if (!CHECK || i < ntok) {
 #pragma unroll
-        for (int c = 0; c < CE; ++c) {
-          dw[0][c] = fmaf(g[c], xt[c], dw[0][c]);
-          dw[1][c] = fmaf(g[c], x1[c], dw[1][c]);
-          dw[2][c] = fmaf(g[c], x2[c], dw[2][c]);
-          dw[3][c] = fmaf(g[c], x3[c], dw[3][c]);
+        for (int c = 0; c < CC / 2; ++c) {
+          dw[0].p[c] = __ffma2_rn(g.p[c], xt.p[c], dw[0].p[c]);
+          dw[1].p[c] = __ffma2_rn(g.p[c], x1.p[c], dw[1].p[c]);
+          dw[2].p[c] = __ffma2_rn(g.p[c], x2.p[c], dw[2].p[c]);
+          dw[3].p[c] = __ffma2_rn(g.p[c], x3.p[c], dw[3].p[c]);
         }
       }
 #pragma unroll
-      for (int c = 0; c < CE; ++c) {
-        y[c] = fmaf(w[3][c], g[c], p3[c]);  // dx of the third token before
-        p3[c] = fmaf(w[2][c], g[c], p2[c]);
-        p2[c] = fmaf(w[1][c], g[c], p1[c]);
-        p1[c] = w[0][c] * g[c];
-        x3[c] = x2[c];
-        x2[c] = x1[c];
-        x1[c] = xt[c];
+      for (int c = 0; c < CC / 2; ++c) {
+        y.p[c] = __ffma2_rn(w[3].p[c], g.p[c], p3.p[c]);  // dx of the third token before
+        p3.p[c] = __ffma2_rn(w[2].p[c], g.p[c], p2.p[c]);
+        p2.p[c] = __ffma2_rn(w[1].p[c], g.p[c], p1.p[c]);
+        p1.p[c] = __fmul2_rn(w[0].p[c], g.p[c]);
       }
-      if (!checked || i - 3 >= lo) put(i - 3, y);
+      x3 = x2;
+      x2 = x1;
+      x1 = xt;
+      if (i - 3 >= lo) {
+        rd.put(y);
+        rd.store(dx + (o - 3 * stride));
+      }
     };
     // What is unfinished before token i is complete where its sequence ends at i.
     auto flush = [&](int i) {
-      if (i - 3 >= lo && i - 3 < ntok) put(i - 3, p3);
-      if (i - 2 >= lo && i - 2 < ntok) put(i - 2, p2);
-      if (i - 1 >= lo && i - 1 < ntok) put(i - 1, p1);
+      auto put = [&](int j, const Pairs<CC> &f) {
+        if (i - j < lo || i - j >= ntok) return;
+        Lane<T, CC> r;
+        r.put(f);
+        r.store(dx + ((unsigned)(i - j) * stride + ch));
+      };
+      put(3, p3);
+      put(2, p2);
+      put(1, p1);
     };
 #pragma unroll
     for (int bt = 0; bt < CS - 1; ++bt) issue(bt);
     int i = 0;
     bool more = true;
     for (int bt = 0; bt < nbatch && more; ++bt) {
+      uint32_t now = 0;  // this batch's scale bytes
+      if (Q)
+#pragma unroll
+        for (int u = 0; u < CU; ++u) now |= (uint32_t)ahead[u] << 8 * u;
       issue(bt + CS - 1);  // into the slot that batch bt - 1 used
       asm volatile("cp.async.wait_group %0;" ::"n"(CS - 1) : "memory");
       const int ib = bt * CU;
-      const uint8_t *slot = ring + (bt % CS) * RB::BYTES;
-      if (ib - 3 >= lo && ib + CU <= ntok && nbr >= ib + CU) {  // a full batch inside one sequence: no checks
+      const uint8_t *slot = ring + (bt % CS) * RB::BATCH;
+      if (ib + CU <= ntok && nbr >= ib + CU) {  // a full batch inside one sequence: no checks
 #pragma unroll
-        for (int u = 0; u < CU; ++u) token(ib + u, u, slot, false);
+        for (int u = 0; u < CU; ++u) token(ib + u, slot + u * RB::TOKEN, act8_unit(now >> 8 * u & 255), std::false_type());
         i = ib + CU;
       } else {
 #pragma unroll 1
@@ -474,21 +480,19 @@ __global__ void __launch_bounds__(CT, 3) prologue_bwd_kernel(const ConvBwdArgs a
             }
             flush(i);
             lo = i;
-#pragma unroll
-            for (int c = 0; c < CE; ++c) x1[c] = x2[c] = x3[c] = p1[c] = p2[c] = p3[c] = 0.f;
-            const long long t = t0 + i;
+            clear();
             if (!a.cu) {
-              nb += a.T;
+              nbr = (int)min((long long)nbr + a.T, (long long)INT_MAX);
             } else {
+              const long long t = t0 + i;
               int m = n + 1;  // cu[m] == t; skip empty sequences
               while (m + 1 < a.N && a.cu[m + 1] <= t) ++m;
               n = m;
               nb = m + 1 <= a.N ? (long long)a.cu[m + 1] : LLONG_MAX;
-              if (nb <= t) nb = LLONG_MAX;
+              nbr = nb <= t ? INT_MAX : (int)min(nb - t0, (long long)INT_MAX);
             }
-            nbr = (int)min(nb - t0, (long long)INT_MAX);
           }
-          token(i, u, slot, true);
+          token(i, slot + u * RB::TOKEN, act8_unit(now >> 8 * u & 255), std::true_type());
           ++i;
         }
       }
@@ -496,46 +500,69 @@ __global__ void __launch_bounds__(CT, 3) prologue_bwd_kernel(const ConvBwdArgs a
     flush(i);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  float *part = a.parts + (size_t)run * a.ncols + P.col + (size_t)ch * K;
 #pragma unroll
-  for (int c = 0; c < CE; ++c)
+  for (int c = 0; c < CC; ++c)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (j < K) part[c * K + K - 1 - j] = dw[j][c];
+      if (j < K) part[c * K + K - 1 - j] = dw[j].get(c);
 }
 
-// Tokens of a run, so that the convolution paths' lanes fill the resident blocks once: at least one
-// load batch, and the same on the host for the workspace's size and the launch.
+template <typename T, typename S>
+__global__ void __launch_bounds__(CT, CONV_BLOCKS) prologue_bwd_kernel(const ConvBwdArgs a) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  // the block's run and path; all of it is uniform in the block but the lane's channel
+  const int per_run = a.path[0].blocks + a.path[1].blocks + a.path[2].blocks;
+  const long long cb = blockIdx.x;
+  if (cb >= a.runs * per_run) {
+    gates_bwd<T, S>(a, (int)(cb - a.runs * per_run));
+    return;
+  }
+  const long long run = cb / per_run;
+  int blk = (int)(cb % per_run), path = 0;
+  while (path < 2 && blk >= a.path[path].blocks) blk -= a.path[path++].blocks;
+  if (path == 2) conv_bwd<T, S, 0>(a, a.path[2], blk, run, ring);
+  else if (a.path[0].dim == 64) conv_bwd<T, S, 64 / CC>(a, a.path[path], blk, run, ring);
+  else conv_bwd<T, S, 128 / CC>(a, a.path[path], blk, run, ring);
+}
+
+// How the work is cut; the same for the workspace's size and the launch.  Runs are as many as let all
+// blocks be resident at once (a second round of a few blocks would double the time), each of at least
+// four tokens and at most what keeps a run's offsets in 32 bits.
 struct ConvBwdPlan {
-  int R;
-  long long runs, blocks[3];
-  int ncols;
+  int threads, blocks[3], R, ncols;
+  long long runs;
 };
-ConvBwdPlan conv_bwd_plan(long long tokens, int H, int dk, int dv, int K, bool bf16) {
+ConvBwdPlan conv_bwd_plan(long long tokens, int H, int dk, int dv, int K) {
   ConvBwdPlan p;
-  const int CU = bf16 ? 4 : 2;
-  const long long lanes = (long long)sm_count() * 3 * CT, work = tokens * H * (long long)(2 * dk + dv) / CE;
-  const long long per = (work + lanes - 1) / lanes;
-  p.R = (int)std::min<long long>(std::max<long long>((per + CU - 1) / CU * CU, CU), 1 << 20);
-  p.runs = (tokens + p.R - 1) / p.R;
+  const long long most = (1ll << 29) / ((long long)H * std::max(dk, dv)) / 4 * 4 - 4;
   const int dim[3] = {dk, dk, dv};
-  for (int i = 0; i < 3; ++i) p.blocks[i] = (p.runs * H * (dim[i] / CE) + CT - 1) / CT;
+  p.threads = (int)std::min<long long>(CT, ((long long)H * std::max(dk, dv) / CC + 31) / 32 * 32);
+  int per_run = 0;
+  for (int i = 0; i < 3; ++i) per_run += p.blocks[i] = (H * dim[i] / CC + p.threads - 1) / p.threads;
+  const long long slots = (long long)sm_count() * CONV_BLOCKS * (CT / p.threads);
+    const long long runs = std::max(1ll, slots * 7 / 8 / per_run), R = ((tokens + runs - 1) / runs + 3) / 4 * 4;
+  p.R = (int)std::min(R, most);
+  p.runs = (tokens + p.R - 1) / p.R;
   p.ncols = H * (2 * dk + dv) * K;
   return p;
 }
 
 template <typename T, typename S>
 cudaError_t prologue_t(const PrologueBwdArgs &p, float *parts, cudaStream_t stream) {
-  const ConvBwdPlan pl = conv_bwd_plan(p.tokens, p.H, p.dk, p.dv, p.K, sizeof(T) == 2);
-  const int dim[6] = {p.dk, p.dk, p.dv, p.dk, p.dk, p.dv};
+  const ConvBwdPlan pl = conv_bwd_plan(p.tokens, p.H, p.dk, p.dv, p.K);
+  const int dim[3] = {p.dk, p.dk, p.dv};
   ConvBwdArgs a{};
   int col = 0;
   ColSumArgs sum{parts, (int)pl.runs, pl.ncols, {}, {}};
   for (int i = 0; i < 3; ++i) {
-    a.conv[i] = ConvBwdPath{p.x[i], p.scales[i], p.W[i], p.d[i], p.dx[i], dim[i], i < 2, col, pl.blocks[i]};
+    const int g = 3 + i;  // alpha with q, b with k, w with v
+    a.path[i] = PathBwd{p.x[i], p.d[i], p.x[g], p.d[g], p.dx[i], p.dx[g], p.scales[i], p.scales[g], p.W[i],
+                        dim[i], i < 2, col, i == 0 ? -1.f : 1.f, pl.blocks[i]};
     col += p.H * dim[i] * p.K;
     sum.out[i] = p.dW[i];
     sum.end[i] = col;
-    a.gate[i] = GateBwdPath{p.x[3 + i], p.scales[3 + i], p.d[3 + i], p.dx[3 + i], dim[3 + i], i == 0 ? -1.f : 1.f};
   }
   a.cu = p.cu;
   a.parts = parts;
@@ -547,14 +574,16 @@ cudaError_t prologue_t(const PrologueBwdArgs &p, float *parts, cudaStream_t stre
   a.R = pl.R;
   a.tokens = p.tokens;
   a.runs = pl.runs;
-  const long long gvec = p.tokens * p.H * (long long)(std::max(p.dk, p.dv) / CE);
-  a.gate_blocks = (int)std::max<long long>(1, std::min<long long>((gvec + 2 * CT - 1) / (2 * CT), (long long)sm_count() * 8));
-  constexpr int smem = CS * Ring<T, S>::BYTES;
-  cudaError_t err = cudaFuncSetAttribute(prologue_bwd_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const long long span = pl.threads * gate_unroll<T>(), rows = p.tokens * p.H;
+  const long long tiles = 2 * ((rows * p.dk / CE + span - 1) / span) + (rows * p.dv / CE + span - 1) / span;
+  a.gate_blocks = (int)std::min<long long>(tiles, (long long)sm_count() * GATE_TILES);
+  constexpr int smem = CS * Ring<T, S>::BATCH;
+  static std::atomic<uint64_t> allowed;
+  cudaError_t err = allow_smem((const void *)prologue_bwd_kernel<T, S>, smem, allowed);
   if (err != cudaSuccess) return err;
-  const long long blocks = pl.blocks[0] + pl.blocks[1] + pl.blocks[2] + a.gate_blocks;
   note_launch();
-  prologue_bwd_kernel<T, S><<<(unsigned)blocks, CT, smem, stream>>>(a);
+  const long long blocks = pl.runs * (pl.blocks[0] + pl.blocks[1] + pl.blocks[2]);
+  prologue_bwd_kernel<T, S><<<(unsigned)(blocks + a.gate_blocks), pl.threads, smem, stream>>>(a);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   return launch_colsum(sum, stream);
 }
@@ -562,7 +591,7 @@ cudaError_t prologue_t(const PrologueBwdArgs &p, float *parts, cudaStream_t stre
 }  // namespace
 
 size_t epilogue_bwd_workspace_bytes(long long rows, int dv) {
-  return (size_t)epilogue_blocks(rows, dv) * dv * sizeof(float);
+  return (size_t)epilogue_blocks(rows, dv, epi_blocks<__nv_bfloat16, int8_t>()) * dv * sizeof(float);
 }
 
 cudaError_t launch_epilogue_bwd(const EpilogueBwdArgs &a, bool bf16, void *ws, cudaStream_t stream) {
@@ -572,8 +601,8 @@ cudaError_t launch_epilogue_bwd(const EpilogueBwdArgs &a, bool bf16, void *ws, c
   return bf16 ? epilogue_t<__nv_bfloat16, __nv_bfloat16>(a, parts, stream) : epilogue_t<float, float>(a, parts, stream);
 }
 
-size_t prologue_bwd_workspace_bytes(long long tokens, int H, int dk, int dv, int K, bool bf16) {
-  const ConvBwdPlan p = conv_bwd_plan(tokens, H, dk, dv, K, bf16);
+size_t prologue_bwd_workspace_bytes(long long tokens, int H, int dk, int dv, int K) {
+  const ConvBwdPlan p = conv_bwd_plan(tokens, H, dk, dv, K);
   return (size_t)p.runs * p.ncols * sizeof(float);
 }
 

@@ -190,11 +190,11 @@ cudaError_t launch_block_epilogue(const BlockEpilogueArgs &p, bool bf16, cudaStr
 cudaError_t launch_act_pack(const ActArgs &a, bool bf16, cudaStream_t stream);
 cudaError_t launch_act_unpack(const ActArgs &a, bool bf16, cudaStream_t stream);
 cudaError_t launch_norm_fwd(const NormFwdArgs &a, bool bf16, cudaStream_t stream);
-size_t norm_bwd_workspace_bytes(long long rows, int width);
+size_t norm_bwd_workspace_bytes(long long rows, int width, bool bf16);
 cudaError_t launch_norm_bwd(const NormBwdArgs &a, bool bf16, void *ws, cudaStream_t stream);
 size_t epilogue_bwd_workspace_bytes(long long rows, int dv);
 cudaError_t launch_epilogue_bwd(const EpilogueBwdArgs &a, bool bf16, void *ws, cudaStream_t stream);
-size_t prologue_bwd_workspace_bytes(long long tokens, int H, int dk, int dv, int K, bool bf16);
+size_t prologue_bwd_workspace_bytes(long long tokens, int H, int dk, int dv, int K);
 cudaError_t launch_prologue_bwd(const PrologueBwdArgs &a, bool bf16, void *ws, cudaStream_t stream);
 
 }  // namespace gdn2

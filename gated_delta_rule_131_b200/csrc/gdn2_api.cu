@@ -454,13 +454,13 @@ gdn2_status gdn2_layer_norm_bwd(const void *dy, const void *h, const uint8_t *h_
     return finish(err);
   }
   const gdn2::NormBwdArgs a{dy, h, h_scales, mean, rstd, weight, dh, dx, dweight, dbias, tokens, width};
-  return finish(with_workspace(gdn2::norm_bwd_workspace_bytes(tokens, width), s,
+  return finish(with_workspace(gdn2::norm_bwd_workspace_bytes(tokens, width, dtype == GDN2_BF16), s,
                                [&](void *ws) { return gdn2::launch_norm_bwd(a, dtype == GDN2_BF16, ws, s); }));
 }
 
-size_t gdn2_layer_norm_bwd_workspace_bytes(long long tokens, int width) {
-  if (tokens <= 0 || width <= 0 || width > gdn2::LN_MAX_WIDTH) return 0;
-  return gdn2::norm_bwd_workspace_bytes(tokens, width);
+size_t gdn2_layer_norm_bwd_workspace_bytes(long long tokens, int width, gdn2_dtype dtype) {
+  if (tokens <= 0 || width <= 0 || width > gdn2::LN_MAX_WIDTH || (dtype != GDN2_F32 && dtype != GDN2_BF16)) return 0;
+  return gdn2::norm_bwd_workspace_bytes(tokens, width, dtype == GDN2_BF16);
 }
 
 gdn2_status gdn2_block_epilogue_bwd(const void *o, const void *gate, const uint8_t *o_scales,
@@ -502,8 +502,8 @@ gdn2_status gdn2_block_prologue_bwd(const void *x_q, const void *x_k, const void
   if (dtype != GDN2_F32 && dtype != GDN2_BF16) return GDN2_ERR_INVALID_ARG;
   if (!supported_dk(d_k) || !supported_dv(d_v) || conv_len < 1 || conv_len > 4) return GDN2_ERR_UNSUPPORTED;
   const long long tokens = cu_seqlens ? (long long)T : (long long)B * T;
-  // the weight gradients of one run of tokens are indexed with 32 bits
-  if (H > INT_MAX / (4 * 512) || !fits(tokens, H, d_v > d_k ? d_v : d_k, 4)) return GDN2_ERR_INVALID_ARG;
+  // a run of tokens is indexed with 32 bits
+  if (H > GDN2_PROLOGUE_BWD_MAX_HEADS || !fits(tokens, H, d_v > d_k ? d_v : d_k, 4)) return GDN2_ERR_INVALID_ARG;
   for (const float *p : {conv_q, conv_k, conv_v, (const float *)dconv_q, (const float *)dconv_k, (const float *)dconv_v})
     if (!p || !aligned4(p)) return GDN2_ERR_INVALID_ARG;
   if (cu_seqlens && !aligned4(cu_seqlens)) return GDN2_ERR_INVALID_ARG;
@@ -525,18 +525,18 @@ gdn2_status gdn2_block_prologue_bwd(const void *x_q, const void *x_k, const void
     return finish(err);
   }
   const bool bf16 = dtype == GDN2_BF16;
-  return finish(with_workspace(gdn2::prologue_bwd_workspace_bytes(tokens, H, d_k, d_v, conv_len, bf16), s,
+  return finish(with_workspace(gdn2::prologue_bwd_workspace_bytes(tokens, H, d_k, d_v, conv_len), s,
                                [&](void *ws) { return gdn2::launch_prologue_bwd(a, bf16, ws, s); }));
 }
 
 size_t gdn2_block_prologue_bwd_workspace_bytes(int B, int T, int H, int d_k, int d_v, int conv_len, int packed,
                                                gdn2_dtype dtype) {
-  if (B <= 0 || T <= 0 || H <= 0 || H > INT_MAX / (4 * 512) || !supported_dk(d_k) || !supported_dv(d_v) ||
+  if (B <= 0 || T <= 0 || H <= 0 || H > GDN2_PROLOGUE_BWD_MAX_HEADS || !supported_dk(d_k) || !supported_dv(d_v) ||
       conv_len < 1 || conv_len > 4 || (dtype != GDN2_F32 && dtype != GDN2_BF16))
     return 0;
   const long long tokens = packed ? (long long)T : (long long)B * T;
   if (!fits(tokens, H, d_v > d_k ? d_v : d_k, 4)) return 0;
-  return gdn2::prologue_bwd_workspace_bytes(tokens, H, d_k, d_v, conv_len, dtype == GDN2_BF16);
+  return gdn2::prologue_bwd_workspace_bytes(tokens, H, d_k, d_v, conv_len);
 }
 
 }  // extern "C"

@@ -7,232 +7,321 @@
 // Backward, with xh = (h - mean) rstd and e = dy g: dx = rstd (e - mean(e) - xh mean(e xh)) + dh,
 // dg = sum over rows of dy xh, db = sum over rows of dy.
 //
-// Both are HBM-bound streams.  A row is held in the registers of one block, NE values per thread, so
-// it is read once; the statistics are two sums over the block, the variance taken about the mean.
+// Both are HBM-bound streams.  A row is held in the registers of `span` threads, NE values each, so it
+// is read once; the statistics are sums over those threads, the variance taken about the mean.  Threads
+// walk rows in turn and load the next one before the sums of this one meet.
 #include <algorithm>
+#include <utility>
 
 #include "act8.cuh"
 
 namespace gdn2 {
 namespace {
 
-constexpr int NE = 16;  // values per thread and row: 512 threads hold LN_MAX_WIDTH of them
-static_assert(512 * NE == LN_MAX_WIDTH, "a block holds the widest row");
+// Calls f(0), f(1), .. with compile-time indices.
+template <typename F, int... I>
+__device__ __forceinline__ void each_(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) { each_(f, std::make_integer_sequence<int, N>()); }
 
-// Threads of a block for a row: whole warps, so that every group of 32 channels lies in one warp.
-int row_threads(int width) { return std::max(1, (width + 32 * NE - 1) / (32 * NE)) * 32; }
-
-// Sums of `a` and `b` over the block, in a fixed order; `red` is one of two buffers used in turn, so
-// one barrier is enough.
-__device__ __forceinline__ void block_sum2(float &a, float &b, float2 *red) {
-  a = warp_allreduce_sum(a);
-  b = warp_allreduce_sum(b);
-  if (blockDim.x == 32) return;
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
-  a = b = 0.f;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
-    a += red[w].x;
-    b += red[w].y;
+// How a row lies in its threads: vector v of thread `tid` covers the VEC columns from (v * span + tid) *
+// VEC, so that a warp's accesses lie side by side and one warp holds every group of 32 channels.  FULL:
+// the row fills its threads, and nothing has to be checked.
+template <int VEC, int NE, bool FULL> struct Row {
+  static constexpr int N = NE / VEC;
+  int D, span, tid;
+  __device__ __forceinline__ int col(int v) const { return (v * span + tid) * VEC; }
+  __device__ __forceinline__ bool inside(int v) const { return FULL || col(v) < D; }
+  // Values past the row's end are zeros.
+  template <typename S> __device__ __forceinline__ void load(LaneVec<S, VEC> (&r)[N], const S *row) const {
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+      if (!FULL) r[v] = LaneVec<S, VEC>{};
+      if (inside(v)) r[v].load(row + col(v));
+    }
   }
+  template <typename S> __device__ __forceinline__ void store(const LaneVec<S, VEC> (&r)[N], S *row) const {
+#pragma unroll
+    for (int v = 0; v < N; ++v)
+      if (inside(v)) r[v].store(row + col(v));
+  }
+  template <typename S> static __device__ __forceinline__ void get(const LaneVec<S, VEC> (&r)[N], Pairs<NE> &f) {
+    each<N>([&](auto v) { widen<v * VEC, VEC>(r[v], f); });
+  }
+  template <typename S> static __device__ __forceinline__ void put(const Pairs<NE> &f, LaneVec<S, VEC> (&r)[N]) {
+    each<N>([&](auto v) { narrow<v * VEC, VEC>(f, r[v]); });
+  }
+  __device__ __forceinline__ void weights(const float *p, Pairs<NE> &f) const {
+    each<N>([&](auto v) {
+      if (inside(v)) load_f32<v * VEC, VEC>(p + col(v), f);
+    });
+  }
+};
+
+// The sums of NV (1 or 2) values over a row's threads, in a fixed order; `group` is the row's place in
+// the block and `red` its block's [warp][2].  A warp folds two values onto its odd and even lanes while
+// it sums.  Two buffers in turn make one barrier enough; each group has its own (0 is __syncthreads').
+template <int NV>
+__device__ __forceinline__ void row_sum(float (&v)[NV], float (*red)[2], int group, int span) {
+  const int lane = threadIdx.x & 31;
+  float s = v[0];
+  if constexpr (NV == 2) {
+    const bool odd = lane & 1;
+    s = (odd ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
+  }
+#pragma unroll
+  for (int m = NV; m < 32; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+  if (span == 32) {
+    if constexpr (NV == 2) v[1] = __shfl_sync(0xffffffffu, s, 1);
+    v[0] = __shfl_sync(0xffffffffu, s, 0);
+    return;
+  }
+  if (lane < NV) red[threadIdx.x >> 5][lane] = s;
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(span) : "memory");
+  const float2 *r = reinterpret_cast<const float2 *>(red[group * (span >> 5)]);
+  float2 t = r[0];
+#pragma unroll 4
+  for (int w = 1; w < span >> 5; ++w) t = __fadd2_rn(t, r[w]);
+  v[0] = t.x;
+  if constexpr (NV == 2) v[1] = t.y;
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, int NE, bool FULL>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwdArgs a) {
-  constexpr int NV = NE / VEC;
-  __shared__ float2 red[2][16];
+  using R = Row<VEC, NE, FULL>;
+  __shared__ __align__(8) float red[2][16][2];
+  const R row{a.width, (int)blockDim.x, (int)threadIdx.x};
   const int D = a.width, groups = (D + ACT_GROUP - 1) / ACT_GROUP;
   const float inv_d = 1.f / (float)D;
-  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const size_t base = (size_t)row * D;
-    LaneVec<T, VEC> rx[NV], rr[NV];
+  const T *px = static_cast<const T *>(a.x), *pr = static_cast<const T *>(a.residual);
+  LaneVec<T, VEC> rx[R::N], rr[R::N];
+  row.load(rx, px + (size_t)blockIdx.x * D);
+  if (pr) row.load(rr, pr + (size_t)blockIdx.x * D);
+  for (long long at = blockIdx.x; at < a.rows; at += gridDim.x) {
+    const size_t base = (size_t)at * D;
+    Pairs<NE> f;
+    R::get(rx, f);
+    if (pr) {
+      Pairs<NE> r;
+      R::get(rr, r);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * VEC;
-      if (c < D) {
-        rx[v] = *reinterpret_cast<const LaneVec<T, VEC> *>(static_cast<const T *>(a.x) + base + c);
-        if (a.residual) rr[v] = *reinterpret_cast<const LaneVec<T, VEC> *>(static_cast<const T *>(a.residual) + base + c);
-      }
+      for (int i = 0; i < NE / 2; ++i) f.p[i] = __fadd2_rn(f.p[i], r.p[i]);
+      R::put(f, rx);
+      row.store(rx, static_cast<T *>(a.h) + base);
+      R::get(rx, f);
     }
-    float f[NV][VEC], sum = 0.f, sq = 0.f, none = 0.f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * VEC;
-      if (c < D) {
-        widen(rx[v], f[v]);
-        if (a.residual) {
-          float r[VEC];
-          widen(rr[v], r);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) f[v][i] += r[i];
-          narrow(f[v], rx[v]);
-          *reinterpret_cast<LaneVec<T, VEC> *>(static_cast<T *>(a.h) + base + c) = rx[v];
-          widen(rx[v], f[v]);
+    if (a.codes)
+      each<R::N>([&](auto v) {
+        uint32_t sc;
+        const LaneVec<int8_t, VEC> code = act8_encode<v * VEC>(rx[v], f, row.inside(v), sc);
+        if (row.inside(v)) {
+          const int c = row.col(v);
+          code.store(a.codes + base + c);
+          if (c % ACT_GROUP == 0) a.scales[(size_t)at * groups + c / ACT_GROUP] = (uint8_t)sc;
         }
+      });
+    if (at + gridDim.x < a.rows) {
+      row.load(rx, px + base + (size_t)gridDim.x * D);
+      if (pr) row.load(rr, pr + base + (size_t)gridDim.x * D);
+    }
+    float s[1] = {total(f)};
+    row_sum(s, red[0], 0, blockDim.x);
+    const float mean = s[0] * inv_d;
+#pragma unroll
+    for (int i = 0; i < NE / 2; ++i) f.p[i] = __fadd2_rn(f.p[i], splat(-mean));
+    if (!FULL) each<R::N>([&](auto v) {
+      if (!row.inside(v))
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f.set(v * VEC + i, 0.f);
+    });
+    s[0] = dot(f, f);
+    row_sum(s, red[1], 0, blockDim.x);
+    const float rstd = 1.f / sqrtf(s[0] * inv_d + a.eps);
+    if (threadIdx.x == 0 && a.mean) {
+      a.mean[at] = mean;
+      a.rstd[at] = rstd;
+    }
+    each<R::N>([&](auto v) {
+      if (!row.inside(v)) return;
+      const int c = row.col(v);
+      Pairs<VEC + VEC % 2> g, b;
+      load_f32<0, VEC>(a.weight + c, g);
+      if (a.bias) load_f32<0, VEC>(a.bias + c, b);
+      else fill(b, 0.f);
+      if constexpr (VEC == 1) {
+        f.set(v, fmaf(f.get(v) * rstd, g.get(0), b.get(0)));
       } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) f[v][i] = 0.f;
+        for (int i = 0; i < VEC / 2; ++i)
+          f.p[v * VEC / 2 + i] = __ffma2_rn(__fmul2_rn(f.p[v * VEC / 2 + i], splat(rstd)), g.p[i], b.p[i]);
       }
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) sum += f[v][i];
-    }
-    if (a.codes) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int c = (v * blockDim.x + threadIdx.x) * VEC;
-        uint32_t s;
-        const LaneVec<int8_t, VEC> q = act8_encode<VEC>(f[v], s);
-        if (c < D) {
-          *reinterpret_cast<LaneVec<int8_t, VEC> *>(a.codes + base + c) = q;
-          if (c % ACT_GROUP == 0) a.scales[(size_t)row * groups + c / ACT_GROUP] = (uint8_t)s;
-        }
-      }
-    }
-    block_sum2(sum, none, red[0]);
-    const float mean = sum * inv_d;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-      if ((v * blockDim.x + threadIdx.x) * VEC < D)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          f[v][i] -= mean;
-          sq = fmaf(f[v][i], f[v][i], sq);
-        }
-    block_sum2(sq, none, red[1]);
-    const float rstd = 1.f / sqrtf(sq * inv_d + a.eps);
-    if (threadIdx.x == 0 && a.mean) {
-      a.mean[row] = mean;
-      a.rstd[row] = rstd;
-    }
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * VEC;
-      if (c < D) {
-        float p[VEC];
-        load_f32(a.weight + c, p);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) f[v][i] *= rstd * p[i];
-        if (a.bias) {
-          load_f32(a.bias + c, p);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) f[v][i] += p[i];
-        }
-        narrow(f[v], rx[v]);
-        *reinterpret_cast<LaneVec<T, VEC> *>(static_cast<T *>(a.y) + base + c) = rx[v];
-      }
-    }
+      LaneVec<T, VEC> y;
+      narrow<v * VEC, VEC>(f, y);
+      y.store(static_cast<T *>(a.y) + base + c);
+    });
   }
 }
 
-// One row of partial sums per block in `parts`: [gridDim.x][2][D] (dweight, dbias).
-template <typename T, typename S, int VEC>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a, float *parts) {
-  constexpr int NV = NE / VEC;
+// A block holds `groups` = blockDim.x / span rows at a time.  The groups' weight gradients are added at
+// the end, so that a block leaves one row of partial sums in `parts`: [gridDim.x][2][D] (dweight, dbias).
+template <typename T, typename S, int VEC, int NE, bool FULL>
+__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a, float *parts, int span) {
   constexpr bool Q = sizeof(S) == 1;  // h is held in 8 bits
-  __shared__ float2 red[2][16];
-  const int D = a.width, groups = (D + ACT_GROUP - 1) / ACT_GROUP;
+  constexpr bool EARLY = NE == 8 || (VEC == 8 && sizeof(T) == 2);  // the registers hold the next row
+  using R = Row<VEC, NE, FULL>;
+  extern __shared__ __align__(16) float sums[];  // [group][2][D], used at the end
+  __shared__ __align__(8) float red[2][16][2];
+  const int D = a.width, scales = (D + ACT_GROUP - 1) / ACT_GROUP;
+  const int group = threadIdx.x / span, groups = blockDim.x / span;
+  const R row{D, span, (int)threadIdx.x - group * span};
   const float inv_d = 1.f / (float)D;
-  float g[NV][VEC], dg[NV][VEC], db[NV][VEC];
+  Pairs<NE> g, dg, db;
+  fill(g, 0.f);
+  fill(dg, 0.f);
+  fill(db, 0.f);
+  if (NE == 8) row.weights(a.weight, g);
+  LaneVec<T, VEC> ry[R::N], rh[R::N];
+  LaneVec<S, VEC> rs[R::N];
+  uint8_t sc[R::N];
+  float mean = 0.f, rstd = 0.f;
+  auto load = [&](long long at) {
+    const size_t base = (size_t)at * D;
+    row.load(ry, static_cast<const T *>(a.dy) + base);
+    row.load(rs, static_cast<const S *>(a.h) + base);
+    if (Q)
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = (v * blockDim.x + threadIdx.x) * VEC;
+      for (int v = 0; v < R::N; ++v)
+        sc[v] = row.inside(v) ? a.scales[(size_t)at * scales + row.col(v) / ACT_GROUP] : 0;
+    mean = a.mean[at];
+    rstd = a.rstd[at];
+  };
+  const long long step = (long long)gridDim.x * groups;
+  long long at = (long long)blockIdx.x * groups + group;
+  if (EARLY && at < a.rows) load(at);
+  for (int turn = 0; at < a.rows; at += step, turn ^= 1) {
+    const size_t base = (size_t)at * D;
+    if (!EARLY) load(at);
+    Pairs<NE> xh, e;
+    if constexpr (Q) each<R::N>([&](auto v) { widen<v * VEC, VEC>(rs[v], act8_unit(sc[v]), xh); });
+    else R::get(rs, xh);
+    R::get(ry, e);
+    if (a.dh) row.load(rh, static_cast<const T *>(a.dh) + base);
+    const float m = -mean, r = rstd;
+    if (at + step < a.rows) load(at + step);
+    if (NE == 16) row.weights(a.weight, g);  // from L1: 8 values fit the registers for good, 16 do not
+    float2 t1 = make_float2(0.f, 0.f), t2 = t1;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) g[v][i] = dg[v][i] = db[v][i] = 0.f;
-    if (c < D) load_f32(a.weight + c, g[v]);
-  }
-  int turn = 0;
-  for (long long row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-    const size_t base = (size_t)row * D;
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    LaneVec<T, VEC> ry[NV], rh[NV];
-    LaneVec<S, VEC> rs[NV];
-    float unit[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * VEC;
-      if (c < D) {
-        ry[v] = *reinterpret_cast<const LaneVec<T, VEC> *>(static_cast<const T *>(a.dy) + base + c);
-        rs[v] = *reinterpret_cast<const LaneVec<S, VEC> *>(static_cast<const S *>(a.h) + base + c);
-        if (Q) unit[v] = act8_unit(a.scales[(size_t)row * groups + c / ACT_GROUP]);
-        if (a.dh) rh[v] = *reinterpret_cast<const LaneVec<T, VEC> *>(static_cast<const T *>(a.dh) + base + c);
-      }
+    for (int i = 0; i < NE / 2; ++i) {
+      xh.p[i] = __fmul2_rn(__fadd2_rn(xh.p[i], splat(m)), splat(r));
+      dg.p[i] = __ffma2_rn(e.p[i], xh.p[i], dg.p[i]);
+      db.p[i] = __fadd2_rn(db.p[i], e.p[i]);
+      e.p[i] = __fmul2_rn(e.p[i], g.p[i]);  // zero past the row's end, and so are its terms below
+      t1 = __fadd2_rn(t1, e.p[i]);
+      t2 = __ffma2_rn(e.p[i], xh.p[i], t2);
     }
-    float xh[NV][VEC], e[NV][VEC], s1 = 0.f, s2 = 0.f;
+    float s[2] = {t1.x + t1.y, t2.x + t2.y};
+    row_sum(s, red[turn], group, span);
+    const float2 k1 = splat(-s[0] * inv_d), k2 = splat(-s[1] * inv_d);
+    if (a.dh) {
+      Pairs<NE> dh;
+      R::get(rh, dh);
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-      if ((v * blockDim.x + threadIdx.x) * VEC < D) {
-        if constexpr (Q) widen(rs[v], unit[v], xh[v]);
-        else widen(rs[v], xh[v]);
-        widen(ry[v], e[v]);
+      for (int i = 0; i < NE / 2; ++i)
+        e.p[i] = __ffma2_rn(splat(r), __ffma2_rn(xh.p[i], k2, __fadd2_rn(e.p[i], k1)), dh.p[i]);
+    } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          xh[v][i] = (xh[v][i] - mean) * rstd;
-          dg[v][i] = fmaf(e[v][i], xh[v][i], dg[v][i]);
-          db[v][i] += e[v][i];
-          e[v][i] *= g[v][i];
-          s1 += e[v][i];
-          s2 = fmaf(e[v][i], xh[v][i], s2);
-        }
-      }
-    block_sum2(s1, s2, red[turn]);
-    s1 *= inv_d;
-    s2 *= inv_d;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * blockDim.x + threadIdx.x) * VEC;
-      if (c < D) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) e[v][i] = rstd * (e[v][i] - s1 - xh[v][i] * s2);
-        if (a.dh) {
-          widen(rh[v], xh[v]);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) e[v][i] += xh[v][i];
-        }
-        narrow(e[v], ry[v]);
-        *reinterpret_cast<LaneVec<T, VEC> *>(static_cast<T *>(a.dx) + base + c) = ry[v];
-      }
+      for (int i = 0; i < NE / 2; ++i)
+        e.p[i] = __fmul2_rn(splat(r), __ffma2_rn(xh.p[i], k2, __fadd2_rn(e.p[i], k1)));
     }
+    R::put(e, rh);
+    row.store(rh, static_cast<T *>(a.dx) + base);
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   float *p = parts + (size_t)blockIdx.x * 2 * D;
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = (v * blockDim.x + threadIdx.x) * VEC;
-    if (c < D) {
-      store_f32(dg[v], p + c);
-      store_f32(db[v], p + D + c);
+  float *mine = groups == 1 ? p : sums + (size_t)group * 2 * D;
+  each<R::N>([&](auto v) {
+    if (row.inside(v)) {
+      store_f32<v * VEC, VEC>(dg, mine + row.col(v));
+      store_f32<v * VEC, VEC>(db, mine + D + row.col(v));
     }
+  });
+  if (groups == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) {
+    float t = sums[c];
+    for (int q = 1; q < groups; ++q) t += sums[(size_t)q * 2 * D + c];
+    p[c] = t;
   }
 }
 
-// Blocks of the backward: enough to fill the GPU, one row at least for each.
-int bwd_blocks(long long rows, int width) {
-  return (int)std::max<long long>(1, std::min<long long>(rows, (long long)sm_count() * std::max(1, 512 / row_threads(width))));
-}
+constexpr int FWD_THREADS = 1024;  // per SM
+static_assert(512 * 16 == LN_MAX_WIDTH, "512 threads hold the widest row");
+// Threads of a row: whole warps of ne values per thread.
+int row_threads(int width, int ne) { return (width + 32 * ne - 1) / (32 * ne) * 32; }
 
-// 16-byte vectors where every row starts on one, single values elsewhere.
-template <typename T>
-bool vector_rows(int width) { return width * sizeof(T) % 16 == 0; }
+template <typename T, int VEC, int NE>
+cudaError_t fwd_launch(const NormFwdArgs &a, cudaStream_t stream) {
+  const int span = row_threads(a.width, NE);
+  const long long fill = (long long)sm_count() * std::min(16, std::max(1, FWD_THREADS / span));
+  const unsigned blocks = (unsigned)std::min<long long>(a.rows, fill);
+  note_launch();
+  if (VEC > 1 && a.width == span * NE) norm_fwd_kernel<T, VEC, NE, true><<<blocks, span, 0, stream>>>(a);
+  else norm_fwd_kernel<T, VEC, NE, false><<<blocks, span, 0, stream>>>(a);
+  return cudaGetLastError();
+}
 
 template <typename T>
 cudaError_t fwd_t(const NormFwdArgs &a, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
-  const unsigned grid = (unsigned)std::min<long long>(a.rows, 1 << 30);
-  const int threads = row_threads(a.width);
+  constexpr int V = 16 / sizeof(T);
+  if (a.width % V == 0) return fwd_launch<T, V, 16>(a, stream);
+  return a.width <= 4096 ? fwd_launch<T, 1, 8>(a, stream) : fwd_launch<T, 1, 16>(a, stream);
+}
+
+// The backward's blocks of up to 512 threads: as many rows at a time as they hold (barriers 1 to 15 are
+// the groups', one warp needs none), one block per SM.
+struct NormBwdPlan {
+  int ne, span, groups, blocks;
+};
+NormBwdPlan norm_bwd_plan(long long rows, int width, bool bf16) {
+  NormBwdPlan p;
+  // 16 values per thread halve the sums' share of the work; fp32 vectors and single values take their
+  // registers twice, and rows that 8 hold are faster so (8192 x 2048 fp32: 51 us, with 16: 66 us)
+  p.ne = width > 4096 || (bf16 && width % 8 == 0) ? 16 : 8;
+  p.span = row_threads(width, p.ne);
+  const int most = p.span == 32 ? 16 : std::min(512 / p.span, 15);
+  const long long sms = sm_count();
+  p.groups = (int)std::max(1ll, std::min<long long>(most, (rows + sms - 1) / sms));
+  p.blocks = (int)std::max(1ll, std::min((rows + p.groups - 1) / p.groups, sms));
+  return p;
+}
+
+template <typename T, typename S, int VEC, int NE>
+cudaError_t bwd_launch(const NormBwdArgs &a, const NormBwdPlan &p, float *parts, cudaStream_t stream) {
+  const int smem = p.groups > 1 ? p.groups * 2 * a.width * (int)sizeof(float) : 0;
+  const bool full = VEC > 1 && a.width == p.span * NE;
+  const auto kernel = full ? norm_bwd_kernel<T, S, VEC, NE, VEC != 1> : norm_bwd_kernel<T, S, VEC, NE, false>;
+  static std::atomic<uint64_t> allowed[2];
+  // at most 512 threads' worth of groups: 512 * NE columns, twice
+  const cudaError_t err = allow_smem((const void *)kernel, 512 * NE * 2 * (int)sizeof(float), allowed[full]);
+  if (err != cudaSuccess) return err;
   note_launch();
-  if (vector_rows<T>(a.width)) norm_fwd_kernel<T, 16 / sizeof(T)><<<grid, threads, 0, stream>>>(a);
-  else norm_fwd_kernel<T, 1><<<grid, threads, 0, stream>>>(a);
+  kernel<<<p.blocks, p.span * p.groups, smem, stream>>>(a, parts, p.span);
   return cudaGetLastError();
 }
 
 template <typename T, typename S>
 cudaError_t bwd_t(const NormBwdArgs &a, float *parts, cudaStream_t stream) {
-  const int blocks = bwd_blocks(a.rows, a.width), threads = row_threads(a.width);
-  note_launch();
-  if (vector_rows<T>(a.width)) norm_bwd_kernel<T, S, 16 / sizeof(T)><<<blocks, threads, 0, stream>>>(a, parts);
-  else norm_bwd_kernel<T, S, 1><<<blocks, threads, 0, stream>>>(a, parts);
-  const cudaError_t err = cudaGetLastError();
+  constexpr int V = 16 / sizeof(T);
+  const NormBwdPlan p = norm_bwd_plan(a.rows, a.width, sizeof(T) == 2);
+  cudaError_t err;
+  if (a.width % V != 0) err = p.ne == 8 ? bwd_launch<T, S, 1, 8>(a, p, parts, stream) : bwd_launch<T, S, 1, 16>(a, p, parts, stream);
+  else if (sizeof(T) == 4 && p.ne == 8) err = bwd_launch<T, S, V, sizeof(T) == 4 ? 8 : 16>(a, p, parts, stream);
+  else err = bwd_launch<T, S, V, 16>(a, p, parts, stream);
   if (err != cudaSuccess) return err;
-  return launch_colsum({parts, blocks, 2 * a.width, {a.dweight, a.dbias, nullptr}, {a.width, 2 * a.width, 2 * a.width}},
+  return launch_colsum({parts, p.blocks, 2 * a.width, {a.dweight, a.dbias, nullptr}, {a.width, 2 * a.width, 2 * a.width}},
                        stream);
 }
 
@@ -242,8 +331,8 @@ cudaError_t launch_norm_fwd(const NormFwdArgs &a, bool bf16, cudaStream_t stream
   return bf16 ? fwd_t<__nv_bfloat16>(a, stream) : fwd_t<float>(a, stream);
 }
 
-size_t norm_bwd_workspace_bytes(long long rows, int width) {
-  return (size_t)bwd_blocks(rows, width) * 2 * width * sizeof(float);
+size_t norm_bwd_workspace_bytes(long long rows, int width, bool bf16) {
+  return (size_t)norm_bwd_plan(rows, width, bf16).blocks * 2 * width * sizeof(float);
 }
 
 cudaError_t launch_norm_bwd(const NormBwdArgs &a, bool bf16, void *ws, cudaStream_t stream) {

@@ -367,7 +367,7 @@ GDN2_API gdn2_status gdn2_layer_norm_bwd(const void *dy, const void *h, const ui
                                          const float *rstd, const float *weight, const void *dh, void *dx,
                                          float *dweight, float *dbias, long long tokens, int width, gdn2_dtype dtype,
                                          gdn2_stream_t stream);
-GDN2_API size_t gdn2_layer_norm_bwd_workspace_bytes(long long tokens, int width);
+GDN2_API size_t gdn2_layer_norm_bwd_workspace_bytes(long long tokens, int width, gdn2_dtype dtype);
 
 /*
  * gdn2_block_epilogue_bwd -- gradients through gdn2_block_epilogue.  Per (token, head), with
@@ -399,11 +399,12 @@ GDN2_API size_t gdn2_block_epilogue_bwd_workspace_bytes(long long tokens, int H,
  *   conv_*     : as in the forward        dq .. dw, dx_q .. dx_w : layouts of x_q .. x_w (dtype)
  *   dconv_q, dconv_k [H * d_k, conv_len], dconv_v [H * d_v, conv_len] : fp32 out, written
  * Layouts (dense, or packed with cu_seqlens), sizes, alignment and errors as for gdn2_block_prologue;
- * H at most INT_MAX / 2048.  In a packed batch T may exceed cu_seqlens[B]: the rows behind the last
+ * H at most GDN2_PROLOGUE_BWD_MAX_HEADS (GDN2_ERR_INVALID_ARG).  In a packed batch T may exceed cu_seqlens[B]: the rows behind the last
  * sequence are not read and their gradients not written.  Outputs must not overlap inputs.  fp32
  * arithmetic; sums in fp32 in a fixed order.  Takes gdn2_block_prologue_bwd_workspace_bytes() bytes
  * from the library's pool.  Without tokens (B == 0 or T == 0) zeros go to dconv_*.
  */
+#define GDN2_PROLOGUE_BWD_MAX_HEADS 65536
 GDN2_API gdn2_status gdn2_block_prologue_bwd(
     const void *x_q, const void *x_k, const void *x_v, const void *x_alpha, const void *x_b, const void *x_w,
     const uint8_t *const *x_scales, const float *conv_q, const float *conv_k, const float *conv_v, const void *dq,

@@ -127,7 +127,7 @@ def test_prologue_bwd_refusals(L):
         assert pro_bwd(L, scales=one) == BAD, i
     assert pro_bwd(L, cu=MIS2) == BAD
     assert pro_bwd(L, B=-1) == BAD and pro_bwd(L, T=-1) == BAD and pro_bwd(L, H=0) == BAD and pro_bwd(L, dtype=4) == BAD
-    assert pro_bwd(L, H=1 << 21) == BAD and pro_bwd(L, B=1 << 30, T=1 << 30, H=1 << 10) == BAD
+    assert pro_bwd(L, H=65537) == BAD and pro_bwd(L, B=1 << 30, T=1 << 30, H=1 << 10) == BAD
     assert pro_bwd(L, K=0) == UNSUP and pro_bwd(L, K=5) == UNSUP
     assert pro_bwd(L, dk=256) == UNSUP and pro_bwd(L, dv=32) == UNSUP
 
@@ -163,9 +163,10 @@ def test_act_refusals(L, name):
 
 def test_workspace_bytes(L):
     """One row of partial weight gradients for each block (148 SMs where there is no GPU)."""
-    assert L.gdn2_layer_norm_bwd_workspace_bytes(1, 100) == 2 * 100 * 4
-    assert L.gdn2_layer_norm_bwd_workspace_bytes(0, 100) == 0
-    assert L.gdn2_layer_norm_bwd_workspace_bytes(5, 8193) == 0
+    assert L.gdn2_layer_norm_bwd_workspace_bytes(1, 100, BF16) == 2 * 100 * 4
+    assert L.gdn2_layer_norm_bwd_workspace_bytes(0, 100, BF16) == 0
+    assert L.gdn2_layer_norm_bwd_workspace_bytes(5, 8193, BF16) == 0
+    assert L.gdn2_layer_norm_bwd_workspace_bytes(5, 64, 7) == 0
     assert L.gdn2_block_epilogue_bwd_workspace_bytes(1, 1, 64) == 64 * 4
     assert L.gdn2_block_epilogue_bwd_workspace_bytes(1, 1, 63) == 0
     n = L.gdn2_block_prologue_bwd_workspace_bytes(1, 2, 1, 64, 128, 3, 0, gdn2.GDN2_F32)
