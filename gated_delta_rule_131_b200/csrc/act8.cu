@@ -79,7 +79,8 @@ __global__ void __launch_bounds__(256) act_unpack_flat_kernel(const ActArgs a) {
   }
 }
 
-// Rows that end inside a group: a warp takes 32 * VEC * NU channels of one row at a time.
+// Rows that end inside a group but start on 16-byte boundaries: a warp takes 32 * VEC * NU channels of
+// one row at a time.
 template <typename T, int VEC, bool PACK>
 __global__ void __launch_bounds__(256) act_rows_kernel(const ActArgs a) {
   constexpr int SPAN = 32 * VEC * NU;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(256) act_rows_kernel(const ActArgs a) {
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       const int c = c0 + u * 32 * VEC;
-      Pairs<VEC + VEC % 2> f;
+      Pairs<VEC> f;
       if constexpr (PACK) {
         widen<0, VEC>(r[u], f);
         uint32_t sc;
@@ -130,6 +131,80 @@ __global__ void __launch_bounds__(256) act_rows_kernel(const ActArgs a) {
   }
 }
 
+// Rows that start anywhere: a warp takes 256 channels of one row at a time, 8 consecutive ones per lane
+// (read one by one, through the L1), so that two shuffles settle a group's scale.  The codes leave as
+// aligned 4-byte words, each put together from two neighbours; only a segment's ragged ends leave as
+// bytes.  (One channel per lane takes five shuffles per channel: 16384 x 1001 bf16, two tensors, 134 us
+// with the reading back; this form 89 us.)
+template <typename T>
+__global__ void __launch_bounds__(256) act_pack_any_kernel(const ActArgs a) {
+  constexpr int V = 8, SPAN = 32 * V;
+  const ActTensor &t = a.t[blockIdx.y];
+  const int per_row = (t.width + SPAN - 1) / SPAN, lane = threadIdx.x & 31;
+  const int groups = (t.width + ACT_GROUP - 1) / ACT_GROUP;
+  const long long tasks = t.rows * per_row, step = (long long)gridDim.x * 8;
+  for (long long k = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); k < tasks; k += step) {
+    const long long row = k / per_row;
+    const int first = (int)(k - row * per_row) * SPAN, c = first + lane * V;
+    const T *x = static_cast<const T *>(t.x) + (size_t)row * t.width + c;
+    LaneVec<T, V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.e[i] = c + i < t.width ? x[i] : T(0.f);
+    Pairs<V> f;
+    widen<0, V>(r, f);
+    uint32_t sc;
+    const LaneVec<int8_t, V> q = act8_encode<0>(r, f, true, sc);
+    if (c < t.width && c % ACT_GROUP == 0) t.scales[(size_t)row * groups + c / ACT_GROUP] = (uint8_t)sc;
+    int8_t *out = t.codes + (size_t)row * t.width + first;
+    const int n = min(SPAN, t.width - first), s = (int)(reinterpret_cast<uintptr_t>(out) & 3);
+    const uint32_t w0 = reinterpret_cast<const uint32_t *>(&q)[0], w1 = reinterpret_cast<const uint32_t *>(&q)[1];
+    const uint32_t before = __shfl_up_sync(0xffffffffu, w1, 1);
+    auto put = [&](int at, uint32_t word) {  // the word of bytes at .. at + 3 of the segment
+      if (at >= 0 && at + 4 <= n) {
+        *reinterpret_cast<uint32_t *>(out + at) = word;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (at + i >= 0 && at + i < n) out[at + i] = (int8_t)(word >> 8 * i);
+      }
+    };
+    put(lane * V - s, __funnelshift_rc(before, w0, 32 - 8 * s));
+    put(lane * V - s + 4, __funnelshift_rc(w0, w1, 32 - 8 * s));
+    if (lane == 31 && s > 0) put(SPAN - s, w1 >> (32 - 8 * s));
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) act_unpack_any_kernel(const ActArgs a) {
+  constexpr int SPAN = 32 * 2 * NU;
+  const ActTensor &t = a.t[blockIdx.y];
+  const int per_row = (t.width + SPAN - 1) / SPAN, lane = threadIdx.x & 31;
+  const int groups = (t.width + ACT_GROUP - 1) / ACT_GROUP;
+  const long long tasks = t.rows * per_row, step = (long long)gridDim.x * 8;
+  for (long long k = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); k < tasks; k += step) {
+    const long long row = k / per_row;
+    const int c0 = (int)(k - row * per_row) * SPAN + lane;
+    const int8_t *codes = t.codes + (size_t)row * t.width;
+    const uint8_t *scales = t.scales + (size_t)row * groups;
+    T *x = static_cast<T *>(t.x) + (size_t)row * t.width;
+    int8_t q[2 * NU];
+    uint8_t s[2 * NU];
+#pragma unroll
+    for (int u = 0; u < 2 * NU; ++u) {
+      const int c = c0 + 32 * u;
+      if (c < t.width) {
+        q[u] = codes[c];
+        s[u] = scales[c / ACT_GROUP];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2 * NU; ++u) {
+      const int c = c0 + 32 * u;
+      if (c < t.width) x[c] = from_f32<T>((float)q[u] * act8_unit(s[u]));
+    }
+  }
+}
+
 // Which kernel serves the call: one launch handles tensors of one kind.  16-byte vectors where every
 // row starts on one (width * element size a multiple of 16), single values elsewhere.
 template <typename T, bool PACK>
@@ -143,7 +218,7 @@ cudaError_t act_t(const ActArgs &all, cudaStream_t stream) {
       const int k = t.width % ACT_GROUP == 0 ? 0 : t.width % V == 0 ? 1 : 2;
       if (k != kind || t.rows == 0) continue;
       a.t[a.count++] = t;
-      const long long span = 32 * NU * (kind == 2 ? 1 : V);
+      const long long span = kind < 2 ? 32 * NU * V : 256;
       most = std::max(most, kind == 0 ? (t.rows * t.width + 8 * span - 1) / (8 * span)
                                       : (t.rows * ((t.width + span - 1) / span) + 7) / 8);
     }
@@ -156,7 +231,8 @@ cudaError_t act_t(const ActArgs &all, cudaStream_t stream) {
     } else if (kind == 1) {
       act_rows_kernel<T, V, PACK><<<grid, 256, 0, stream>>>(a);
     } else {
-      act_rows_kernel<T, 1, PACK><<<grid, 256, 0, stream>>>(a);
+      if (PACK) act_pack_any_kernel<T><<<grid, 256, 0, stream>>>(a);
+      else act_unpack_any_kernel<T><<<grid, 256, 0, stream>>>(a);
     }
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;

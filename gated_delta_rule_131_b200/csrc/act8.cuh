@@ -54,28 +54,55 @@ template <int N> __device__ __forceinline__ float dot(const Pairs<N> &a, const P
   return s.x + s.y;
 }
 
+// 32 bytes at once (on a 32-byte boundary), marked first to leave the L2 where STREAM.
+struct alignas(32) Words8 { uint32_t w[8]; };
+template <bool STREAM> __device__ __forceinline__ Words8 load32(const void *p) {
+  Words8 v;
+  if constexpr (STREAM)
+    asm volatile("ld.global.cs.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+                 : "l"(p) : "memory");
+  else
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+                 : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store32(void *p, const Words8 &v) {
+  asm volatile("st.global.cs.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v.w[0]), "r"(v.w[1]), "r"(v.w[2]),
+               "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]), "r"(v.w[7])
+               : "memory");
+}
+
 // VEC consecutive values of one lane, in memory.  Streams are read and written once: `load` and
 // `store` mark their lines first to leave the L2.
 template <typename T, int VEC> struct alignas(sizeof(T) * VEC) LaneVec {
   T e[VEC];
   static constexpr int BYTES = sizeof(T) * VEC;
   __device__ __forceinline__ void load(const T *p) {
-    if constexpr (BYTES == 16) *reinterpret_cast<uint4 *>(this) = __ldcs(reinterpret_cast<const uint4 *>(p));
+    if constexpr (BYTES == 32) *reinterpret_cast<Words8 *>(this) = load32<true>(p);
+    else if constexpr (BYTES == 16) *reinterpret_cast<uint4 *>(this) = __ldcs(reinterpret_cast<const uint4 *>(p));
     else if constexpr (BYTES == 8) *reinterpret_cast<uint2 *>(this) = __ldcs(reinterpret_cast<const uint2 *>(p));
     else if constexpr (BYTES == 4) *reinterpret_cast<uint32_t *>(this) = __ldcs(reinterpret_cast<const uint32_t *>(p));
     else if constexpr (BYTES == 2) *reinterpret_cast<uint16_t *>(this) = __ldcs(reinterpret_cast<const uint16_t *>(p));
     else *reinterpret_cast<uint8_t *>(this) = __ldcs(reinterpret_cast<const uint8_t *>(p));
   }
   // The same through the L1 as usual.
-  __device__ __forceinline__ void load_cached(const T *p) { *this = *reinterpret_cast<const LaneVec *>(p); }
+  __device__ __forceinline__ void load_cached(const T *p) {
+    if constexpr (BYTES == 32) *reinterpret_cast<Words8 *>(this) = load32<false>(p);
+    else *this = *reinterpret_cast<const LaneVec *>(p);
+  }
   __device__ __forceinline__ void store(T *p) const {
-    if constexpr (BYTES == 16) __stcs(reinterpret_cast<uint4 *>(p), *reinterpret_cast<const uint4 *>(this));
+    if constexpr (BYTES == 32) store32(p, *reinterpret_cast<const Words8 *>(this));
+    else if constexpr (BYTES == 16) __stcs(reinterpret_cast<uint4 *>(p), *reinterpret_cast<const uint4 *>(this));
     else if constexpr (BYTES == 8) __stcs(reinterpret_cast<uint2 *>(p), *reinterpret_cast<const uint2 *>(this));
     else if constexpr (BYTES == 4) __stcs(reinterpret_cast<uint32_t *>(p), *reinterpret_cast<const uint32_t *>(this));
     else if constexpr (BYTES == 2) __stcs(reinterpret_cast<uint16_t *>(p), *reinterpret_cast<const uint16_t *>(this));
     else __stcs(reinterpret_cast<uint8_t *>(p), *reinterpret_cast<const uint8_t *>(this));
   }
 };
+// Whether every one of the given pointers lies on a 32-byte boundary.
+template <typename... P> inline bool on32(const P *...p) { return ((reinterpret_cast<uintptr_t>(p) | ...) & 31u) == 0; }
 
 // Values AT .. AT + VEC - 1 of `f` from a lane's vector; codes are multiplied by their group's unit.
 template <int AT, int VEC, int N>
@@ -140,9 +167,10 @@ template <int VEC>
 __device__ __forceinline__ uint32_t amax_bits(const LaneVec<__nv_bfloat16, VEC> &r) {
   if constexpr (VEC % 2 == 0) {  // two 15-bit patterns to a word
     const uint32_t *w = reinterpret_cast<const uint32_t *>(&r);
-    static_assert(VEC == 8, "four words");
-    uint32_t m = __vimax3_s16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu, w[2] & 0x7fff7fffu);
-    m = __vimax3_s16x2(m, m, w[3] & 0x7fff7fffu);
+    uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int i = 1; i < VEC / 2; i += 2)
+      m = __vimax3_s16x2(m, w[i] & 0x7fff7fffu, w[i + 1 < VEC / 2 ? i + 1 : i] & 0x7fff7fffu);
     return max(m & 0xffff0000u, m << 16);
   } else {
     return (uint32_t)(__bfloat16_as_ushort(r.e[0]) & 0x7fffu) << 16;

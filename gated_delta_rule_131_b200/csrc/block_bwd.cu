@@ -39,9 +39,9 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
 // 1 - s of a pair.
 __device__ __forceinline__ float2 one_minus2(float2 s) { return __ffma2_rn(s, splat(-1.f), splat(1.f)); }
 
-// N channels of a lane, as loaded: words of 16 bytes at most.
-template <typename S, int N> struct Lane {
-  static constexpr int VEC = sizeof(S) == 4 ? 4 : N, WORDS = N / VEC;
+// N channels of a lane, as loaded: words of WB bytes at most (16, or 32 on such boundaries).
+template <typename S, int N, int WB = 16> struct Lane {
+  static constexpr int VEC = N * (int)sizeof(S) > WB ? WB / (int)sizeof(S) : N, WORDS = N / VEC;
   LaneVec<S, VEC> v[WORDS];
   __device__ __forceinline__ void load(const S *p) {
 #pragma unroll
@@ -55,17 +55,14 @@ template <typename S, int N> struct Lane {
 #pragma unroll
     for (int i = 0; i < WORDS; ++i) v[i].store(p + i * VEC);
   }
-  __device__ __forceinline__ void get(Pairs<N> &f, float unit) const {
-    if constexpr (sizeof(S) == 1) {
-      widen<0, VEC>(v[0], unit, f);
-    } else {
-      widen<0, VEC>(v[0], f);
-      if constexpr (WORDS == 2) widen<VEC, VEC>(v[1], f);
-    }
+  template <int I = 0> __device__ __forceinline__ void get(Pairs<N> &f, float unit) const {
+    if constexpr (sizeof(S) == 1) widen<I * VEC, VEC>(v[I], unit, f);
+    else widen<I * VEC, VEC>(v[I], f);
+    if constexpr (I + 1 < WORDS) get<I + 1>(f, unit);
   }
-  __device__ __forceinline__ void put(const Pairs<N> &f) {
-    narrow<0, VEC>(f, v[0]);
-    if constexpr (WORDS == 2) narrow<VEC, VEC>(f, v[1]);
+  template <int I = 0> __device__ __forceinline__ void put(const Pairs<N> &f) {
+    narrow<I * VEC, VEC>(f, v[I]);
+    if constexpr (I + 1 < WORDS) put<I + 1>(f);
   }
 };
 
@@ -105,31 +102,25 @@ __device__ __forceinline__ void cp_async(void *smem, const void *gmem) {
 // dy oh s.  A row of d_v values is held by G = d_v / 8 lanes, 8 per lane; groups of lanes take rows in
 // turn and keep their dg in registers.  HBM-bound: each value is read once and written once.
 
-// Blocks per SM: what 128 (fp32), 80 (bf16) or 64 registers (bf16 from 8 bits: its loads are half as wide,
-// and a fourth block pays for a few spills: 162 us instead of 171 on 12345 x 32 x 256) allow.
-constexpr int EPI_THREADS = 256;
-template <typename T, typename S> __host__ __device__ constexpr int epi_blocks() {
-  return sizeof(T) == 4 ? 2 : sizeof(S) == 1 ? 4 : 3;
-}
+constexpr int EC = 16;  // channels per lane
+constexpr int EPI_THREADS = 256, EPI_BLOCKS = 2;  // blocks per SM: 128 registers
 
-template <typename T, typename S, int DV>
-__global__ void __launch_bounds__(EPI_THREADS, epi_blocks<T, S>()) epilogue_bwd_kernel(const EpilogueBwdArgs a, float *parts) {
-  constexpr int G = DV / CE, GROUPS = EPI_THREADS / G, TILE = EPI_THREADS * CE;  // whole rows
+template <typename T, typename S, int DV, int WB>
+__global__ void __launch_bounds__(EPI_THREADS, EPI_BLOCKS) epilogue_bwd_kernel(const EpilogueBwdArgs a, float *parts) {
+  constexpr int G = DV / EC, GROUPS = EPI_THREADS / G, TILE = EPI_THREADS * EC;  // whole rows
   constexpr bool Q = sizeof(S) == 1;
   __shared__ float red[GROUPS][DV];
-  const int grp = threadIdx.x / G, c = (threadIdx.x % G) * CE;
-  const unsigned off = threadIdx.x * CE;  // a lane's place in every tile
-  Pairs<CE> g, dg;
+  const int grp = threadIdx.x / G, c = (threadIdx.x % G) * EC;
+  const unsigned off = threadIdx.x * EC;  // a lane's place in every tile
+  Pairs<EC> g, dg;
   fill(dg, 0.f);
 #pragma unroll
-  for (int i = 0; i < CE; ++i) g.set(i, a.g[c + i]);
+  for (int i = 0; i < EC; ++i) g.set(i, a.g[c + i]);
   const long long total = a.rows * DV, step = (long long)gridDim.x * TILE;
-  Lane<S, CE> ro, rz;
-  Lane<T, CE> ry;
+  Lane<S, EC, WB> ro, rz;
+  Lane<T, EC, WB> ry;
   uint8_t so = 0, sz = 0;
-  auto inside = [&](long long base) { return off < (unsigned)min(total - base, (long long)TILE); };
   auto load = [&](long long base) {  // (marked to leave the L2 first, the loads cost 3 % here)
-    if (!inside(base)) return;
     ro.load_cached(static_cast<const S *>(a.o) + base + off);
     rz.load_cached(static_cast<const S *>(a.z) + base + off);
     ry.load_cached(static_cast<const T *>(a.dy) + base + off);
@@ -138,11 +129,10 @@ __global__ void __launch_bounds__(EPI_THREADS, epi_blocks<T, S>()) epilogue_bwd_
       sz = a.z_scales[base / ACT_GROUP + off / ACT_GROUP];
     }
   };
-  long long base = (long long)blockIdx.x * TILE;
-  load(base);
-  for (; base < total; base += step) {
-    const bool live = inside(base);
-    Pairs<CE> o, z, e;
+  auto inside = [&](long long base) { return base + off < total; };
+  auto tile = [&](long long base, auto checked) {
+    const bool live = !decltype(checked)::value || inside(base);
+    Pairs<EC> o, z, e;
     if (live) {
       ro.get(o, Q ? act8_unit(so) : 0.f);
       rz.get(z, Q ? act8_unit(sz) : 0.f);
@@ -152,10 +142,10 @@ __global__ void __launch_bounds__(EPI_THREADS, epi_blocks<T, S>()) epilogue_bwd_
       fill(z, 0.f);
       fill(e, 0.f);
     }
-    if (base + step < total) load(base + step);
+    if (inside(base + step)) load(base + step);
     const float r = rsqrt_approx(row_sum<G>(dot(o, o)) * (1.f / DV) + RMS_EPS);
 #pragma unroll
-    for (int i = 0; i < CE / 2; ++i) {
+    for (int i = 0; i < EC / 2; ++i) {
       const float2 sg = sigmoid2(z.p[i]), s = __fmul2_rn(z.p[i], sg);
       o.p[i] = __fmul2_rn(o.p[i], splat(r));  // oh
       const float2 yo = __fmul2_rn(e.p[i], o.p[i]), yg = __fmul2_rn(e.p[i], g.p[i]);
@@ -166,17 +156,21 @@ __global__ void __launch_bounds__(EPI_THREADS, epi_blocks<T, S>()) epilogue_bwd_
     const float m = row_sum<G>(dot(e, o)) * (-1.f / DV);
     if (live) {
 #pragma unroll
-      for (int i = 0; i < CE / 2; ++i) e.p[i] = __fmul2_rn(splat(r), __ffma2_rn(o.p[i], splat(m), e.p[i]));
-      Lane<T, CE> out;
+      for (int i = 0; i < EC / 2; ++i) e.p[i] = __fmul2_rn(splat(r), __ffma2_rn(o.p[i], splat(m), e.p[i]));
+      Lane<T, EC, WB> out;
       out.put(e);
       out.store(static_cast<T *>(a.dout) + base + off);
       out.put(z);
       out.store(static_cast<T *>(a.dz) + base + off);
     }
-  }
+  };
+  long long base = (long long)blockIdx.x * TILE;
+  if (inside(base)) load(base);
+  for (; base + TILE <= total; base += step) tile(base, std::false_type());
+  if (base < total) tile(base, std::true_type());
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < CE; ++i) red[grp][c + i] = dg.get(i);
+  for (int i = 0; i < EC; ++i) red[grp][c + i] = dg.get(i);
   __syncthreads();
   for (int k = threadIdx.x; k < DV; k += EPI_THREADS) {
     float s = 0.f;
@@ -186,21 +180,28 @@ __global__ void __launch_bounds__(EPI_THREADS, epi_blocks<T, S>()) epilogue_bwd_
   }
 }
 
-int epilogue_blocks(long long rows, int dv, int per_sm) {
-  const long long per = EPI_THREADS / (dv / CE), most = (long long)sm_count() * per_sm;
+int epilogue_blocks(long long rows, int dv) {
+  const long long per = EPI_THREADS / (dv / EC), most = (long long)sm_count() * EPI_BLOCKS;
   return (int)std::max(1ll, std::min((rows + per - 1) / per, most));
+}
+
+template <typename T, typename S, int WB>
+cudaError_t epilogue_t(const EpilogueBwdArgs &a, float *parts, cudaStream_t stream) {
+  const int blocks = epilogue_blocks(a.rows, a.dv);
+  note_launch();
+  if (a.dv == 64) epilogue_bwd_kernel<T, S, 64, WB><<<blocks, EPI_THREADS, 0, stream>>>(a, parts);
+  else if (a.dv == 128) epilogue_bwd_kernel<T, S, 128, WB><<<blocks, EPI_THREADS, 0, stream>>>(a, parts);
+  else epilogue_bwd_kernel<T, S, 256, WB><<<blocks, EPI_THREADS, 0, stream>>>(a, parts);
+  const cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  return launch_colsum({parts, blocks, a.dv, {a.dg, nullptr, nullptr}, {a.dv, a.dv, a.dv}}, stream);
 }
 
 template <typename T, typename S>
 cudaError_t epilogue_t(const EpilogueBwdArgs &a, float *parts, cudaStream_t stream) {
-  const int blocks = epilogue_blocks(a.rows, a.dv, epi_blocks<T, S>());
-  note_launch();
-  if (a.dv == 64) epilogue_bwd_kernel<T, S, 64><<<blocks, EPI_THREADS, 0, stream>>>(a, parts);
-  else if (a.dv == 128) epilogue_bwd_kernel<T, S, 128><<<blocks, EPI_THREADS, 0, stream>>>(a, parts);
-  else epilogue_bwd_kernel<T, S, 256><<<blocks, EPI_THREADS, 0, stream>>>(a, parts);
-  const cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  return launch_colsum({parts, blocks, a.dv, {a.dg, nullptr, nullptr}, {a.dv, a.dv, a.dv}}, stream);
+  const bool wide = on32((const char *)a.dy, (const char *)a.dout, (const char *)a.dz, sizeof(S) == 1 ? nullptr : (const char *)a.o,
+                         sizeof(S) == 1 ? nullptr : (const char *)a.z);
+  return wide ? epilogue_t<T, S, 32>(a, parts, stream) : epilogue_t<T, S, 16>(a, parts, stream);
 }
 
 // ---------------------------------------------------------------------------------------- prologue
@@ -591,7 +592,7 @@ cudaError_t prologue_t(const PrologueBwdArgs &p, float *parts, cudaStream_t stre
 }  // namespace
 
 size_t epilogue_bwd_workspace_bytes(long long rows, int dv) {
-  return (size_t)epilogue_blocks(rows, dv, epi_blocks<__nv_bfloat16, int8_t>()) * dv * sizeof(float);
+  return (size_t)epilogue_blocks(rows, dv) * dv * sizeof(float);
 }
 
 cudaError_t launch_epilogue_bwd(const EpilogueBwdArgs &a, bool bf16, void *ws, cudaStream_t stream) {

@@ -58,6 +58,26 @@ template <int VEC, int NE, bool FULL> struct Row {
       if (inside(v)) load_f32<v * VEC, VEC>(p + col(v), f);
     });
   }
+  // The row's weights, kept in shared memory as [NE / 4][span] float4 where a lane's vector is longer
+  // than one: read from there they cost no bank conflicts, while a warp's 16-byte loads 32 or 64 bytes
+  // apart would take the L1 twice or four times as long (backward 8192 x 2048: 34 us instead of 32).
+  static constexpr bool STAGED = VEC > 4;
+  __device__ __forceinline__ void stage(const float *p, float4 *s) const {
+    Pairs<NE> f;
+    fill(f, 0.f);
+    weights(p, f);
+#pragma unroll
+    for (int k = 0; k < NE / 4; ++k)
+      s[k * span + tid] = make_float4(f.p[2 * k].x, f.p[2 * k].y, f.p[2 * k + 1].x, f.p[2 * k + 1].y);
+  }
+  __device__ __forceinline__ void staged(const float4 *s, Pairs<NE> &f) const {
+#pragma unroll
+    for (int k = 0; k < NE / 4; ++k) {
+      const float4 q = s[k * span + tid];
+      f.p[2 * k] = make_float2(q.x, q.y);
+      f.p[2 * k + 1] = make_float2(q.z, q.w);
+    }
+  }
 };
 
 // The sums of NV (1 or 2) values over a row's threads, in a fixed order; `group` is the row's place in
@@ -88,6 +108,7 @@ __device__ __forceinline__ void row_sum(float (&v)[NV], float (*red)[2], int gro
   if constexpr (NV == 2) v[1] = t.y;
 }
 
+// One row at a time per block.
 template <typename T, int VEC, int NE, bool FULL>
 __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwdArgs a) {
   using R = Row<VEC, NE, FULL>;
@@ -169,9 +190,9 @@ __global__ void __launch_bounds__(512) norm_fwd_kernel(const NormFwdArgs a) {
 template <typename T, typename S, int VEC, int NE, bool FULL>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a, float *parts, int span) {
   constexpr bool Q = sizeof(S) == 1;  // h is held in 8 bits
-  constexpr bool EARLY = NE == 8 || (VEC == 8 && sizeof(T) == 2);  // the registers hold the next row
+  constexpr bool EARLY = NE == 8 || (VEC > 1 && sizeof(T) == 2);  // the registers hold the next row
   using R = Row<VEC, NE, FULL>;
-  extern __shared__ __align__(16) float sums[];  // [group][2][D], used at the end
+  extern __shared__ __align__(16) float sums[];  // the weights where R::STAGED; at the end [group][2][D]
   __shared__ __align__(8) float red[2][16][2];
   const int D = a.width, scales = (D + ACT_GROUP - 1) / ACT_GROUP;
   const int group = threadIdx.x / span, groups = blockDim.x / span;
@@ -181,7 +202,12 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a, floa
   fill(g, 0.f);
   fill(dg, 0.f);
   fill(db, 0.f);
-  if (NE == 8) row.weights(a.weight, g);
+  if (R::STAGED) {
+    if (group == 0) row.stage(a.weight, reinterpret_cast<float4 *>(sums));
+    __syncthreads();
+  } else if (NE == 8) {
+    row.weights(a.weight, g);
+  }
   LaneVec<T, VEC> ry[R::N], rh[R::N];
   LaneVec<S, VEC> rs[R::N];
   uint8_t sc[R::N];
@@ -210,7 +236,8 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a, floa
     if (a.dh) row.load(rh, static_cast<const T *>(a.dh) + base);
     const float m = -mean, r = rstd;
     if (at + step < a.rows) load(at + step);
-    if (NE == 16) row.weights(a.weight, g);  // from L1: 8 values fit the registers for good, 16 do not
+    if constexpr (R::STAGED) row.staged(reinterpret_cast<const float4 *>(sums), g);
+    else if (NE == 16) row.weights(a.weight, g);  // 8 values fit the registers for good, 16 do not
     float2 t1 = make_float2(0.f, 0.f), t2 = t1;
 #pragma unroll
     for (int i = 0; i < NE / 2; ++i) {
@@ -241,6 +268,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdArgs a, floa
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   float *p = parts + (size_t)blockIdx.x * 2 * D;
   float *mine = groups == 1 ? p : sums + (size_t)group * 2 * D;
+  if (R::STAGED && groups > 1) __syncthreads();  // every group has read its last weights
   each<R::N>([&](auto v) {
     if (row.inside(v)) {
       store_f32<v * VEC, VEC>(dg, mine + row.col(v));
@@ -261,23 +289,24 @@ static_assert(512 * 16 == LN_MAX_WIDTH, "512 threads hold the widest row");
 // Threads of a row: whole warps of ne values per thread.
 int row_threads(int width, int ne) { return (width + 32 * ne - 1) / (32 * ne) * 32; }
 
-template <typename T, int VEC, int NE>
+template <typename T, int VEC, int NE, bool FULL>
 cudaError_t fwd_launch(const NormFwdArgs &a, cudaStream_t stream) {
   const int span = row_threads(a.width, NE);
   const long long fill = (long long)sm_count() * std::min(16, std::max(1, FWD_THREADS / span));
-  const unsigned blocks = (unsigned)std::min<long long>(a.rows, fill);
   note_launch();
-  if (VEC > 1 && a.width == span * NE) norm_fwd_kernel<T, VEC, NE, true><<<blocks, span, 0, stream>>>(a);
-  else norm_fwd_kernel<T, VEC, NE, false><<<blocks, span, 0, stream>>>(a);
+  norm_fwd_kernel<T, VEC, NE, FULL><<<(unsigned)std::min<long long>(a.rows, fill), span, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
+// 16-byte vectors where every row starts on one, else single values.  (32-byte vectors, which the
+// backward takes, are no faster here: 8192 x 2048 with a residual 25 us either way.)
 template <typename T>
 cudaError_t fwd_t(const NormFwdArgs &a, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
   constexpr int V = 16 / sizeof(T);
-  if (a.width % V == 0) return fwd_launch<T, V, 16>(a, stream);
-  return a.width <= 4096 ? fwd_launch<T, 1, 8>(a, stream) : fwd_launch<T, 1, 16>(a, stream);
+  if (a.width % (32 * 16) == 0) return fwd_launch<T, V, 16, true>(a, stream);
+  if (a.width % V == 0) return fwd_launch<T, V, 16, false>(a, stream);
+  return a.width <= 4096 ? fwd_launch<T, 1, 8, false>(a, stream) : fwd_launch<T, 1, 16, false>(a, stream);
 }
 
 // The backward's blocks of up to 512 threads: as many rows at a time as they hold (barriers 1 to 15 are
@@ -298,28 +327,35 @@ NormBwdPlan norm_bwd_plan(long long rows, int width, bool bf16) {
   return p;
 }
 
-template <typename T, typename S, int VEC, int NE>
+template <typename T, typename S, int VEC, int NE, bool FULL>
 cudaError_t bwd_launch(const NormBwdArgs &a, const NormBwdPlan &p, float *parts, cudaStream_t stream) {
-  const int smem = p.groups > 1 ? p.groups * 2 * a.width * (int)sizeof(float) : 0;
-  const bool full = VEC > 1 && a.width == p.span * NE;
-  const auto kernel = full ? norm_bwd_kernel<T, S, VEC, NE, VEC != 1> : norm_bwd_kernel<T, S, VEC, NE, false>;
-  static std::atomic<uint64_t> allowed[2];
+  const auto kernel = norm_bwd_kernel<T, S, VEC, NE, FULL>;
+  static std::atomic<uint64_t> allowed;
   // at most 512 threads' worth of groups: 512 * NE columns, twice
-  const cudaError_t err = allow_smem((const void *)kernel, 512 * NE * 2 * (int)sizeof(float), allowed[full]);
+  const cudaError_t err = allow_smem((const void *)kernel, 512 * NE * 2 * (int)sizeof(float), allowed);
   if (err != cudaSuccess) return err;
   note_launch();
+  const int smem = std::max(p.groups > 1 ? p.groups * 2 * a.width : 0, VEC > 4 ? p.span * NE : 0) * (int)sizeof(float);
   kernel<<<p.blocks, p.span * p.groups, smem, stream>>>(a, parts, p.span);
   return cudaGetLastError();
 }
 
+// 32-byte vectors where a row fills its threads and everything lies on such boundaries (half the
+// instructions for loads and addresses: 8192 x 2048 in 32 us, 37 us without), 16-byte ones where every
+// row starts on one, else single values.
 template <typename T, typename S>
 cudaError_t bwd_t(const NormBwdArgs &a, float *parts, cudaStream_t stream) {
-  constexpr int V = 16 / sizeof(T);
+  constexpr int V = 16 / sizeof(T), FEW = sizeof(T) == 4 ? 8 : 16;  // see norm_bwd_plan
   const NormBwdPlan p = norm_bwd_plan(a.rows, a.width, sizeof(T) == 2);
+  const bool full = a.width % (32 * p.ne) == 0 &&
+                    on32((const char *)a.dy, (const char *)a.dh, (const char *)a.dx, a.scales ? nullptr : (const char *)a.h);
   cudaError_t err;
-  if (a.width % V != 0) err = p.ne == 8 ? bwd_launch<T, S, 1, 8>(a, p, parts, stream) : bwd_launch<T, S, 1, 16>(a, p, parts, stream);
-  else if (sizeof(T) == 4 && p.ne == 8) err = bwd_launch<T, S, V, sizeof(T) == 4 ? 8 : 16>(a, p, parts, stream);
-  else err = bwd_launch<T, S, V, 16>(a, p, parts, stream);
+  if (a.width % V != 0)
+    err = p.ne == 8 ? bwd_launch<T, S, 1, 8, false>(a, p, parts, stream) : bwd_launch<T, S, 1, 16, false>(a, p, parts, stream);
+  else if (p.ne == FEW)
+    err = full ? bwd_launch<T, S, 2 * V, FEW, true>(a, p, parts, stream) : bwd_launch<T, S, V, FEW, false>(a, p, parts, stream);
+  else
+    err = full ? bwd_launch<T, S, 2 * V, 16, true>(a, p, parts, stream) : bwd_launch<T, S, V, 16, false>(a, p, parts, stream);
   if (err != cudaSuccess) return err;
   return launch_colsum({parts, p.blocks, 2 * a.width, {a.dweight, a.dbias, nullptr}, {a.width, 2 * a.width, 2 * a.width}},
                        stream);

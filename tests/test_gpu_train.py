@@ -197,6 +197,39 @@ def test_layer_norm_bwd(g, dtype, width, ckpt, along):
     assert g.layer_norm_bwd(dy, held, out.mean, out.rstd, w, dh=dh, want_dbias=False)[2] is None
 
 
+def off16(t):
+    """A copy of ``t`` that starts on a 16-byte boundary and on no 32-byte one."""
+    buf = torch.empty(t.numel() + 16 // t.element_size(), dtype=t.dtype, device=t.device)
+    v = buf[16 // t.element_size():].view(t.shape)
+    assert v.data_ptr() % 32 == 16
+    return v.copy_(t)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width", [512, 2048, 8192])
+@pytest.mark.parametrize("ckpt", [False, True])
+def test_layer_norm_on_16_byte_boundaries(g, dtype, width, ckpt):
+    """Rows that would move in 32-byte vectors, on pointers that forbid it."""
+    tokens = 300
+    h, dy, dh = (off16(rand(i, tokens, width, dtype=dtype)) for i in (1, 2, 3))
+    w = off16(rand(4, width, scale=0.3, shift=1.0))
+    out = g.layer_norm_fwd(h, w, off16(rand(5, width)), residual=dh)
+    ref = g.layer_norm_fwd(h.clone(), w.clone(), rand(5, width), residual=dh.clone())
+    assert torch.equal(out.y, ref.y) and torch.equal(out.h, ref.h) and torch.equal(out.rstd, ref.rstd)
+    held, h64 = hold(g, h, ckpt)
+    if ckpt:
+        held = g.Act8(off16(held.codes), off16(held.scales))
+    n = g.layer_norm_fwd(h, w)
+    dx, dw, db = g.layer_norm_bwd(dy, held, n.mean, n.rstd, w, dh=dh)
+    mean, rstd, w64, dy64 = np64(n.mean), np64(n.rstd), np64(w), np64(dy)
+    rx, rw, rb = bt.layer_norm_bwd(dy64, h64, mean, rstd, w64, np64(dh))
+    axh, ae = np.abs(h64 - mean[:, None]) * rstd[:, None], np.abs(dy64 * w64)
+    major = rstd[:, None] * (ae + ae.mean(-1, keepdims=True) + axh * (ae * axh).mean(-1, keepdims=True))
+    close(dx, rx, major + np.abs(np64(dh)), C_ROW, "dx")
+    close(dw, rw, (np.abs(dy64) * axh).sum(0), C_SUM, "dweight")
+    close(db, rb, np.abs(dy64).sum(0), C_SUM, "dbias")
+
+
 def test_layer_norm_gradient_against_differences(g):
     """fp32: the gradient along a random direction, against central differences of the fp64 forward."""
     h, w, b, dy = rand(1, 23, 200), rand(2, 200), rand(3, 200), rand(4, 23, 200)
@@ -253,6 +286,24 @@ def test_epilogue_bwd(g, dtype, dv, tokens, H, ckpt):
     close(dg, rg, (np.abs(dy64) * aoh * s).sum((0, 1)), C_SUM, "dnorm_weight")
     again = g.block_epilogue_bwd(oh_, zh, nw, dy)
     assert all(torch.equal(p, q) for p, q in zip((do, dz, dg), again))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("ckpt", [False, True])
+def test_block_backwards_on_16_byte_boundaries(g, dtype, ckpt):
+    """The same results on pointers that are 16-byte but not 32-byte aligned."""
+    hand = (lambda t: g.Act8(*[off16(p) for p in g.act_pack(t)])) if ckpt else off16
+    held = g.act_pack if ckpt else (lambda t: t)
+    o, z, dy = (rand(i, 130, 3, 128, dtype=dtype) for i in (1, 2, 3))
+    nw = rand(4, 128)
+    for p, q in zip(g.block_epilogue_bwd(hand(o), hand(z), off16(nw), off16(dy)),
+                    g.block_epilogue_bwd(held(o), held(z), nw, dy)):
+        assert torch.equal(p, q)
+    t = [rand(10 + i, 2, 60, 2, 64, dtype=dtype) for i in range(12)]
+    conv = [rand(30 + i, 128, 4) for i in range(3)]
+    for p, q in zip(g.block_prologue_bwd(*[hand(x) for x in t[:6]], *[off16(c) for c in conv], *[off16(d) for d in t[6:]]),
+                    g.block_prologue_bwd(*[held(x) for x in t[:6]], *conv, *t[6:])):
+        assert torch.equal(p, q)
 
 
 def test_epilogue_bwd_without_tokens_zero_rows_and_far_gates(g):
