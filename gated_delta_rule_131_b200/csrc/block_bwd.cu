@@ -215,13 +215,15 @@ cudaError_t epilogue_t(const EpilogueBwdArgs &a, float *parts, cudaStream_t stre
 // A block holds up to 512 neighbouring channels of one path, 4 per lane, so that d / 4 lanes hold one
 // (token, head) row, and walks a run of R tokens forwards.  dx_t is complete once dy_{t+K-1} is known, so three unfinished dx and the
 // three previous x stay in registers beside the taps and their gradients; each run walks K - 1 tokens
-// further than it writes.  The taps' gradients of a run leave as one row of partial sums.  Every lane
+// further than it writes.  The taps' gradients of a run leave as one row of partial sums; within it
+// they are sums of sums over 256 tokens, so that a long run's rounding does not grow with its length.  Every lane
 // also takes the gate of its path's width (alpha with q, b with k, w with v) at the same offsets: the
 // gates are pure traffic, the convolutions mostly arithmetic, and so the two overlap.
 
 constexpr int CT = 128;           // threads of a block, at most
 constexpr int CONV_BLOCKS = 4;    // blocks of that many threads per SM
 constexpr int GATE_TILES = 32;    // blocks of the gates per SM, at most
+constexpr int SUM_BATCHES = 64;   // load batches after which the taps' gradients move to their second level
 constexpr int CS = 2;             // load batches in a lane's ring (one is used, the other in flight)
 
 struct PathBwd {  // a convolution path and the gate that goes with it
@@ -297,7 +299,8 @@ __device__ __forceinline__ void gates_bwd(const ConvBwdArgs &a, int block) {
 
 // One block's run of one path; G: lanes of a row whose norm is taken, 0 for a path without one.
 template <typename T, typename S, int G>
-__device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P, int blk, long long run, uint8_t *ring) {
+__device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P, int blk, long long run, uint8_t *ring,
+                                         float4 (*far)[CT]) {
   using RB = Ring<T, S>;
   constexpr int CU = RB::CU;
   constexpr bool Q = sizeof(S) == 1;
@@ -317,7 +320,19 @@ __device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P,
     fill(dw[j], 0.f);
 #pragma unroll
     for (int i = 0; i < CC; ++i) w[j].set(i, j < K ? P.W[(size_t)(ch + i) * K + K - 1 - j] : 0.f);
+    far[j][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  auto second_level = [&] {  // far += dw, a lane's own words only
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float4 s = far[j][threadIdx.x];
+      s.x += dw[j].p[0].x;
+      s.y += dw[j].p[0].y;
+      s.z += dw[j].p[1].x;
+      s.w += dw[j].p[1].y;
+      far[j][threadIdx.x] = s;
+    }
+  };
   const int ntok = (int)max(0ll, min((long long)a.R, live - t0));           // tokens of the run
   const int nload = (int)max(0ll, min((long long)a.R + K - 1, live - t0));  // and those its dx reach
   if (ntok > 0) {
@@ -461,6 +476,11 @@ __device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P,
       if (Q)
 #pragma unroll
         for (int u = 0; u < CU; ++u) now |= (uint32_t)ahead[u] << 8 * u;
+      if (bt % SUM_BATCHES == SUM_BATCHES - 1) {
+        second_level();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fill(dw[j], 0.f);
+      }
       issue(bt + CS - 1);  // into the slot that batch bt - 1 used
       asm volatile("cp.async.wait_group %0;" ::"n"(CS - 1) : "memory");
       const int ib = bt * CU;
@@ -502,17 +522,22 @@ __device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P,
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  second_level();
   float *part = a.parts + (size_t)run * a.ncols + P.col + (size_t)ch * K;
 #pragma unroll
-  for (int c = 0; c < CC; ++c)
+  for (int j = 0; j < 4; ++j) {
+    const float4 q = far[j][threadIdx.x];
+    const float s[CC] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < K) part[c * K + K - 1 - j] = dw[j].get(c);
+    for (int c = 0; c < CC; ++c)
+      if (j < K) part[c * K + K - 1 - j] = s[c];
+  }
 }
 
 template <typename T, typename S>
 __global__ void __launch_bounds__(CT, CONV_BLOCKS) prologue_bwd_kernel(const ConvBwdArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float4 far[4][CT];
   // the block's run and path; all of it is uniform in the block but the lane's channel
   const int per_run = a.path[0].blocks + a.path[1].blocks + a.path[2].blocks;
   const long long cb = blockIdx.x;
@@ -523,9 +548,9 @@ __global__ void __launch_bounds__(CT, CONV_BLOCKS) prologue_bwd_kernel(const Con
   const long long run = cb / per_run;
   int blk = (int)(cb % per_run), path = 0;
   while (path < 2 && blk >= a.path[path].blocks) blk -= a.path[path++].blocks;
-  if (path == 2) conv_bwd<T, S, 0>(a, a.path[2], blk, run, ring);
-  else if (a.path[0].dim == 64) conv_bwd<T, S, 64 / CC>(a, a.path[path], blk, run, ring);
-  else conv_bwd<T, S, 128 / CC>(a, a.path[path], blk, run, ring);
+  if (path == 2) conv_bwd<T, S, 0>(a, a.path[2], blk, run, ring, far);
+  else if (a.path[0].dim == 64) conv_bwd<T, S, 64 / CC>(a, a.path[path], blk, run, ring, far);
+  else conv_bwd<T, S, 128 / CC>(a, a.path[path], blk, run, ring, far);
 }
 
 // How the work is cut; the same for the workspace's size and the launch.  Runs are as many as let all
