@@ -26,7 +26,6 @@ Entry points (same names as the C ABI):
   bits between the forward and the backward pass (``gdn2_act_pack``,
   ``gdn2_act_unpack``), which the backward calls read directly.
 """
-import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional
@@ -391,49 +390,42 @@ class LayerNormOut(NamedTuple):
     checkpoint: Optional[Act8]
 
 
-class _launching:
-    """Makes the device of ``tensors`` and the launch stream current: outputs are allocated for that
-    stream, and inputs are kept until its work is done.  Enters with the stream's handle."""
-    __slots__ = ("tensors", "stream", "guards")
-
-    def __init__(self, stream, *tensors):
-        self.tensors, self.stream, self.guards = tensors, stream, None
-
-    def __enter__(self):
-        dev = None
-        for t in self.tensors:
-            if t is None:
-                continue
+def _handle(tensors):
+    """The handle of the current stream, or None where the tensors' device is not the current one.
+    (Everything on this path is paid by every call, short ones too, so it is kept plain.)"""
+    dev = None
+    for t in tensors:
+        if t is not None:
             d = t.get_device()
-            if d < 0:
-                raise ValueError("gdn2: all tensors must be CUDA tensors")
-            if dev is None:
+            if d != dev:
+                if d < 0:
+                    raise ValueError("gdn2: all tensors must be CUDA tensors")
+                if dev is not None:
+                    raise ValueError("gdn2: tensors on different devices")
                 dev = d
-            elif d != dev:
-                raise ValueError("gdn2: tensors on different devices")
             if not t.is_contiguous():
                 raise ValueError("gdn2: all tensors must be contiguous")
-        if self.stream is None and dev == torch.cuda.current_device():  # nothing to switch
-            return torch._C._cuda_getCurrentRawStream(dev)
-        self.guards = contextlib.ExitStack()
-        self.guards.enter_context(torch.cuda.device(dev))
-        if self.stream is None or self.stream == torch.cuda.current_stream(dev):
-            self.stream = None
-        elif self.stream.device.index != dev:
-            self.guards.close()
-            raise ValueError("gdn2: the stream is on another device than the tensors")
-        else:
-            self.guards.enter_context(torch.cuda.stream(self.stream))
-        return torch._C._cuda_getCurrentRawStream(dev)
+    if dev != torch.cuda.current_device():
+        return None
+    return torch._C._cuda_getCurrentRawStream(dev)
 
-    def __exit__(self, *exc):
-        if self.guards is not None:
-            self.guards.close()
-            if self.stream is not None:
-                for t in self.tensors:
-                    if t is not None:
-                        t.record_stream(self.stream)
-        return False
+
+def _elsewhere(stream, tensors, call):
+    """``call()`` with the tensors' device and ``stream`` (None: that device's current one) made current:
+    outputs are allocated for that stream, and inputs are kept until its work is done."""
+    tensors = [t for t in tensors if t is not None]
+    _check_tensors(*tensors)
+    dev = tensors[0].device
+    if stream is not None and stream.device != dev:
+        raise ValueError("gdn2: the stream is on another device than the tensors")
+    with torch.cuda.device(dev):
+        if stream is None or stream == torch.cuda.current_stream(dev):
+            return call()
+        with torch.cuda.stream(stream):
+            out = call()
+        for t in tensors:
+            t.record_stream(stream)
+        return out
 
 
 def _expect(what, name, t, dtype, shape):
@@ -468,14 +460,20 @@ def _saved(what, name, x, like):
     return x, None
 
 
-def _act_call(entry, first, second, third, shaped, dtype, stream):
-    n = len(shaped)
-    vps = ctypes.c_void_p * n
-    width = [t.shape[-1] for t in shaped]
-    st = getattr(lib(), entry)(vps(*[t.data_ptr() for t in first]), vps(*[t.data_ptr() for t in second]),
-                               vps(*[t.data_ptr() for t in third]),
-                               (ctypes.c_longlong * n)(*[t.numel() // w for t, w in zip(shaped, width)]),
-                               (ctypes.c_int * n)(*width), n, _DTYPES[dtype], stream)
+_HOST_ARRAYS = [(ctypes.c_void_p * n, ctypes.c_longlong * n, ctypes.c_int * n) for n in range(ACT_MAX_TENSORS + 1)]
+
+
+def _act_call(entry, first, second, third, dtype, stream):
+    """``first`` holds tensors of the shapes of the values."""
+    n = len(first)
+    if n > ACT_MAX_TENSORS:
+        raise Gdn2Error(GDN2_ERR_UNSUPPORTED, entry)
+    pointers, longs, ints = _HOST_ARRAYS[n]
+    width = [t.shape[-1] for t in first]
+    st = getattr(lib(), entry)(pointers(*[t.data_ptr() for t in first]), pointers(*[t.data_ptr() for t in second]),
+                               pointers(*[t.data_ptr() for t in third]),
+                               longs(*[t.numel() // w for t, w in zip(first, width)]), ints(*width), n,
+                               _DTYPES[dtype], stream)
     if st != GDN2_OK:
         raise Gdn2Error(st, entry)
 
@@ -493,9 +491,11 @@ def act_pack(xs, stream=None):
             raise ValueError("gdn2: act_pack: the tensors must share dtype float32 or bfloat16")
         if x.dim() < 1 or x.shape[-1] < 1:
             raise ValueError("gdn2: act_pack: a tensor needs a last dimension of at least 1")
-    with _launching(stream, *xs) as s:
-        out = [_new_act8(x) for x in xs]
-        _act_call("gdn2_act_pack", xs, [a.codes for a in out], [a.scales for a in out], xs, dtype, s)
+    s = _handle(xs) if stream is None else None
+    if s is None:
+        return _elsewhere(stream, xs, lambda: act_pack(xs[0] if one else xs))
+    out = [_new_act8(x) for x in xs]
+    _act_call("gdn2_act_pack", xs, [a.codes for a in out], [a.scales for a in out], dtype, s)
     return out[0] if one else out
 
 
@@ -512,9 +512,11 @@ def act_unpack(acts, dtype=torch.bfloat16, stream=None):
             raise ValueError("gdn2: act_unpack: a tensor needs a last dimension of at least 1")
         _check_act8("act_unpack", "act", a, a.codes.shape)
     codes, scales = [a.codes for a in acts], [a.scales for a in acts]
-    with _launching(stream, *codes, *scales) as s:
-        out = [torch.empty_like(c, dtype=dtype) for c in codes]
-        _act_call("gdn2_act_unpack", codes, scales, out, out, dtype, s)
+    s = _handle(codes + scales) if stream is None else None
+    if s is None:
+        return _elsewhere(stream, codes + scales, lambda: act_unpack(acts[0] if one else acts, dtype))
+    out = [torch.empty_like(c, dtype=dtype) for c in codes]
+    _act_call("gdn2_act_unpack", codes, scales, out, dtype, s)
     return out[0] if one else out
 
 
@@ -534,22 +536,24 @@ def layer_norm_fwd(x, weight, bias=None, residual=None, eps=1e-5, checkpoint=Fal
     _expect(what, "residual", residual, dtype, shape)
     _expect(what, "weight", weight, torch.float32, (D,))
     _expect(what, "bias", bias, torch.float32, (D,))
-    with _launching(stream, x, weight, bias, residual) as s:
-        y = torch.empty_like(x)
-        h = mean = rstd = ck = codes = scales = None
-        if residual is not None:
-            h = torch.empty_like(x)
-        if stats:
-            mean = x.new_empty(shape[:-1], dtype=torch.float32)
-            rstd = torch.empty_like(mean)
-        if checkpoint:
-            ck = _new_act8(x)
-            codes, scales = ck
-        st = lib().gdn2_layer_norm_fwd(x.data_ptr(), _addr(residual), weight.data_ptr(), _addr(bias), eps, y.data_ptr(),
-                                       _addr(h), _addr(mean), _addr(rstd), _addr(codes), _addr(scales), x.numel() // D,
-                                       D, _DTYPES[dtype], s)
-        if st != GDN2_OK:
-            raise Gdn2Error(st, "gdn2_layer_norm_fwd")
+    tensors = (x, weight, bias, residual)
+    s = _handle(tensors) if stream is None else None
+    if s is None:
+        return _elsewhere(stream, tensors, lambda: layer_norm_fwd(x, weight, bias, residual, eps, checkpoint, stats))
+    y = torch.empty_like(x)
+    h = mean = rstd = ck = codes = scales = None
+    if residual is not None:
+        h = torch.empty_like(x)
+    if stats:
+        mean = x.new_empty(shape[:-1], dtype=torch.float32)
+        rstd = torch.empty_like(mean)
+    if checkpoint:
+        codes, scales = ck = _new_act8(x)
+    st = lib().gdn2_layer_norm_fwd(x.data_ptr(), _addr(residual), weight.data_ptr(), _addr(bias), eps, y.data_ptr(),
+                                   _addr(h), _addr(mean), _addr(rstd), _addr(codes), _addr(scales), x.numel() // D, D,
+                                   _DTYPES[dtype], s)
+    if st != GDN2_OK:
+        raise Gdn2Error(st, "gdn2_layer_norm_fwd")
     return LayerNormOut(y, x if h is None else h, mean, rstd, ck)
 
 
@@ -571,14 +575,17 @@ def layer_norm_bwd(dy, h, mean, rstd, weight, dh=None, want_dbias=True, stream=N
     _expect(what, "rstd", rstd, torch.float32, shape[:-1])
     _expect(what, "weight", weight, torch.float32, (D,))
     values, scales = _saved(what, "h", h, dy)
-    with _launching(stream, dy, values, scales, mean, rstd, weight, dh) as s:
-        dx, dweight = torch.empty_like(dy), torch.empty_like(weight)
-        dbias = torch.empty_like(weight) if want_dbias else None
-        st = lib().gdn2_layer_norm_bwd(dy.data_ptr(), values.data_ptr(), _addr(scales), mean.data_ptr(),
-                                       rstd.data_ptr(), weight.data_ptr(), _addr(dh), dx.data_ptr(),
-                                       dweight.data_ptr(), _addr(dbias), dy.numel() // D, D, _DTYPES[dtype], s)
-        if st != GDN2_OK:
-            raise Gdn2Error(st, "gdn2_layer_norm_bwd")
+    tensors = (dy, values, scales, mean, rstd, weight, dh)
+    s = _handle(tensors) if stream is None else None
+    if s is None:
+        return _elsewhere(stream, tensors, lambda: layer_norm_bwd(dy, h, mean, rstd, weight, dh, want_dbias))
+    dx, dweight = torch.empty_like(dy), torch.empty_like(weight)
+    dbias = torch.empty_like(weight) if want_dbias else None
+    st = lib().gdn2_layer_norm_bwd(dy.data_ptr(), values.data_ptr(), _addr(scales), mean.data_ptr(), rstd.data_ptr(),
+                                   weight.data_ptr(), _addr(dh), dx.data_ptr(), dweight.data_ptr(), _addr(dbias),
+                                   dy.numel() // D, D, _DTYPES[dtype], s)
+    if st != GDN2_OK:
+        raise Gdn2Error(st, "gdn2_layer_norm_bwd")
     return dx, dweight, dbias
 
 
@@ -604,13 +611,16 @@ def block_epilogue_bwd(o, gate, norm_weight, dy, stream=None):
     _expect(what, "norm_weight", norm_weight, torch.float32, (dv,))
     oc, osc = _saved(what, "o", o, dy)
     gc, gsc = _saved(what, "gate", gate, dy)
-    with _launching(stream, oc, osc, gc, gsc, norm_weight, dy) as s:
-        do, dgate, dnorm_weight = torch.empty_like(dy), torch.empty_like(dy), torch.empty_like(norm_weight)
-        st = lib().gdn2_block_epilogue_bwd(oc.data_ptr(), gc.data_ptr(), _addr(osc), _addr(gsc), norm_weight.data_ptr(),
-                                           dy.data_ptr(), do.data_ptr(), dgate.data_ptr(), dnorm_weight.data_ptr(),
-                                           dy.numel() // (H * dv), H, dv, _DTYPES[dtype], s)
-        if st != GDN2_OK:
-            raise Gdn2Error(st, "gdn2_block_epilogue_bwd")
+    tensors = (oc, osc, gc, gsc, norm_weight, dy)
+    s = _handle(tensors) if stream is None else None
+    if s is None:
+        return _elsewhere(stream, tensors, lambda: block_epilogue_bwd(o, gate, norm_weight, dy))
+    do, dgate, dnorm_weight = torch.empty_like(dy), torch.empty_like(dy), torch.empty_like(norm_weight)
+    st = lib().gdn2_block_epilogue_bwd(oc.data_ptr(), gc.data_ptr(), _addr(osc), _addr(gsc), norm_weight.data_ptr(),
+                                       dy.data_ptr(), do.data_ptr(), dgate.data_ptr(), dnorm_weight.data_ptr(),
+                                       dy.numel() // (H * dv), H, dv, _DTYPES[dtype], s)
+    if st != GDN2_OK:
+        raise Gdn2Error(st, "gdn2_block_epilogue_bwd")
     return do, dgate, dnorm_weight
 
 
@@ -650,30 +660,31 @@ def block_prologue_bwd(xq, xk, xv, xa, xb, xw, conv_q, conv_k, conv_v, dq, dk, d
         B = cu_seqlens.numel() - 1
         T, H, d_k = shape
     d_v, K = dv.shape[-1], conv_q.shape[1]
-    vshape = (*shape[:-1], d_v)
-    for name, t, expect in zip(("dq", "dk", "dv", "dalpha", "db", "dw"), grads,
-                               (shape, shape, vshape, shape, shape, vshape)):
-        _expect(what, name, t, dtype, expect)
-    for name, t, d in zip(("conv_q", "conv_k", "conv_v"), convs, (d_k, d_k, d_v)):
-        _expect(what, name, t, torch.float32, (H * d, K))
-    if packed8:
-        for name, x, t in zip(_PRE, xs, grads):
-            _check_act8(what, name, x, t.shape)
-        saved, scale_list = [x.codes for x in xs], [x.scales for x in xs]
-    else:
-        for name, x, t in zip(_PRE, xs, grads):
-            _expect(what, name, x, dtype, t.shape)
-        saved, scale_list = xs, ()
-    with _launching(stream, *grads, *saved, *scale_list, *convs, cu_seqlens) as s:
-        dxs = [torch.empty_like(t) for t in grads]
-        dconv = [torch.empty_like(t) for t in convs]
-        scales = (ctypes.c_void_p * 6)(*[t.data_ptr() for t in scale_list]) if packed8 else None
-        st = lib().gdn2_block_prologue_bwd(*[t.data_ptr() for t in saved], scales, *[t.data_ptr() for t in convs],
-                                           *[t.data_ptr() for t in grads], *[t.data_ptr() for t in dxs],
-                                           *[t.data_ptr() for t in dconv], B, T, H, d_k, d_v, K, _addr(cu_seqlens),
-                                           _DTYPES[dtype], s)
-        if st != GDN2_OK:
-            raise Gdn2Error(st, "gdn2_block_prologue_bwd")
+    vshape = torch.Size((*shape[:-1], d_v))
+    shapes = (shape, shape, vshape, shape, shape, vshape)
+    for i in range(6):
+        if grads[i].dtype is not dtype or grads[i].shape != shapes[i]:
+            _expect(what, ("dq", "dk", "dv", "dalpha", "db", "dw")[i], grads[i], dtype, shapes[i])
+        if packed8:
+            _check_act8(what, _PRE[i], xs[i], shapes[i])
+        elif xs[i].dtype is not dtype or xs[i].shape != shapes[i]:
+            _expect(what, _PRE[i], xs[i], dtype, shapes[i])
+    for i, d in enumerate((d_k, d_k, d_v)):
+        _expect(what, ("conv_q", "conv_k", "conv_v")[i], convs[i], torch.float32, (H * d, K))
+    saved, scale_list = ([x.codes for x in xs], [x.scales for x in xs]) if packed8 else (xs, ())
+    tensors = (*grads, *saved, *scale_list, *convs, cu_seqlens)
+    s = _handle(tensors) if stream is None else None
+    if s is None:
+        return _elsewhere(stream, tensors, lambda: block_prologue_bwd(*xs, *convs, *grads, cu_seqlens=cu_seqlens))
+    dxs = [torch.empty_like(t) for t in grads]
+    dconv = [torch.empty_like(t) for t in convs]
+    scales = _HOST_ARRAYS[6][0](*[t.data_ptr() for t in scale_list]) if packed8 else None
+    st = lib().gdn2_block_prologue_bwd(*[t.data_ptr() for t in saved], scales, *[t.data_ptr() for t in convs],
+                                       *[t.data_ptr() for t in grads], *[t.data_ptr() for t in dxs],
+                                       *[t.data_ptr() for t in dconv], B, T, H, d_k, d_v, K, _addr(cu_seqlens),
+                                       _DTYPES[dtype], s)
+    if st != GDN2_OK:
+        raise Gdn2Error(st, "gdn2_block_prologue_bwd")
     return (*dxs, *dconv)
 
 

@@ -102,12 +102,12 @@ __device__ __forceinline__ void cp_async(void *smem, const void *gmem) {
 // dy oh s.  A row of d_v values is held by G = d_v / 8 lanes, 8 per lane; groups of lanes take rows in
 // turn and keep their dg in registers.  HBM-bound: each value is read once and written once.
 
-constexpr int EC = 16;  // channels per lane
-constexpr int EPI_THREADS = 256, EPI_BLOCKS = 2;  // blocks per SM: 128 registers
+template <typename T> constexpr int EPI_CHANNELS = 32 / sizeof(T);  // per lane: one 32-byte vector
+constexpr int EPI_THREADS = 256, EPI_BLOCKS = 2;                    // blocks per SM: 128 registers
 
 template <typename T, typename S, int DV, int WB>
 __global__ void __launch_bounds__(EPI_THREADS, EPI_BLOCKS) epilogue_bwd_kernel(const EpilogueBwdArgs a, float *parts) {
-  constexpr int G = DV / EC, GROUPS = EPI_THREADS / G, TILE = EPI_THREADS * EC;  // whole rows
+  constexpr int EC = EPI_CHANNELS<T>, G = DV / EC, GROUPS = EPI_THREADS / G, TILE = EPI_THREADS * EC;  // whole rows
   constexpr bool Q = sizeof(S) == 1;
   __shared__ float red[GROUPS][DV];
   const int grp = threadIdx.x / G, c = (threadIdx.x % G) * EC;
@@ -180,14 +180,14 @@ __global__ void __launch_bounds__(EPI_THREADS, EPI_BLOCKS) epilogue_bwd_kernel(c
   }
 }
 
-int epilogue_blocks(long long rows, int dv) {
-  const long long per = EPI_THREADS / (dv / EC), most = (long long)sm_count() * EPI_BLOCKS;
+int epilogue_blocks(long long rows, int dv, int channels) {
+  const long long per = EPI_THREADS / (dv / channels), most = (long long)sm_count() * EPI_BLOCKS;
   return (int)std::max(1ll, std::min((rows + per - 1) / per, most));
 }
 
 template <typename T, typename S, int WB>
 cudaError_t epilogue_t(const EpilogueBwdArgs &a, float *parts, cudaStream_t stream) {
-  const int blocks = epilogue_blocks(a.rows, a.dv);
+  const int blocks = epilogue_blocks(a.rows, a.dv, EPI_CHANNELS<T>);
   note_launch();
   if (a.dv == 64) epilogue_bwd_kernel<T, S, 64, WB><<<blocks, EPI_THREADS, 0, stream>>>(a, parts);
   else if (a.dv == 128) epilogue_bwd_kernel<T, S, 128, WB><<<blocks, EPI_THREADS, 0, stream>>>(a, parts);
@@ -617,7 +617,7 @@ cudaError_t prologue_t(const PrologueBwdArgs &p, float *parts, cudaStream_t stre
 }  // namespace
 
 size_t epilogue_bwd_workspace_bytes(long long rows, int dv) {
-  return (size_t)epilogue_blocks(rows, dv) * dv * sizeof(float);
+  return (size_t)epilogue_blocks(rows, dv, EPI_CHANNELS<float>) * dv * sizeof(float);
 }
 
 cudaError_t launch_epilogue_bwd(const EpilogueBwdArgs &a, bool bf16, void *ws, cudaStream_t stream) {
