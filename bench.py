@@ -241,7 +241,7 @@ def main():
     ap.add_argument("--no-bwd", action="store_true", help="skip the backward measurement")
     ap.add_argument("--no-workloads", action="store_true",
                     help="skip the long-context, sequence-length sweep and packed-varlen measurements")
-    ap.add_argument("--profile-case", choices=["chunk", "decode", "block", "bwd", "bwd_small"],
+    ap.add_argument("--profile-case", choices=["chunk", "decode", "block", "bwd", "bwd_small", "train"],
                     help="run one warm-up and one measured launch of that kernel on its full workload, for ncu")
     args = ap.parse_args()
     args.warmup = max(args.warmup, 3)
@@ -381,6 +381,23 @@ def profile_case(which):
         for _ in range(2):
             gdn2.block_prologue(*[d[n] for n in ("xq", "xk", "xv", "xa", "xb", "xw", "conv_q", "conv_k", "conv_v")])
             gdn2.block_epilogue(d["xv"], d["z"], d["norm_weight"])
+    elif which == "train":  # the block's training operators, in their type and from 8-bit checkpoints
+        wl = W.WORKLOADS["layer_1p3b"]
+        d = W.block_inputs(wl, device=dev, seed=0, conv_len=4)
+        pre, conv = [d[n] for n in ("xq", "xk", "xv", "xa", "xb", "xw")], [d[n] for n in ("conv_q", "conv_k", "conv_v")]
+        rows = [d[n].reshape(wl.B, wl.T, -1) for n in ("xq", "xk")]  # any [.., 2048] rows serve the norm here
+        weight = torch.ones(rows[0].shape[-1], device=dev)
+        grads = [t.flip(0).contiguous() for t in pre]
+        for _ in range(2):
+            n = gdn2.layer_norm_fwd(rows[0], weight, weight, residual=rows[1], checkpoint=True)
+            gdn2.layer_norm_bwd(rows[1], n.h, n.mean, n.rstd, weight, dh=rows[0])
+            gdn2.layer_norm_bwd(rows[1], n.checkpoint, n.mean, n.rstd, weight, dh=rows[0])
+            gdn2.block_epilogue_bwd(d["xv"], d["z"], d["norm_weight"], d["xw"])
+            gdn2.block_prologue_bwd(*pre, *conv, *grads)
+            held = gdn2.act_pack([*pre, d["z"]])
+            gdn2.block_epilogue_bwd(held[2], held[6], d["norm_weight"], d["xw"])
+            gdn2.block_prologue_bwd(*held[:6], *conv, *grads)
+            gdn2.act_unpack(held)
     else:
         wl = W.WORKLOADS["decode"]
         S = W.decode_state(wl, device=dev, seed=0)

@@ -99,8 +99,15 @@ __device__ __forceinline__ void cp_async(void *smem, const void *gmem) {
 //
 // y = oh g s with oh = o r, r = 1 / sqrt(mean o^2 + eps), s = z sigmoid(z).  With e = dy g s:
 // do = r (e - oh mean(e oh)), dz = dy g oh sigmoid(z) (1 + z (1 - sigmoid(z))), dg = sum over rows of
-// dy oh s.  A row of d_v values is held by G = d_v / 8 lanes, 8 per lane; groups of lanes take rows in
-// turn and keep their dg in registers.  HBM-bound: each value is read once and written once.
+// dy oh s.
+//
+// A row of d_v values is held by G lanes, one 32-byte vector of dy each (16 bf16 or 8 fp32 values); a
+// block takes tiles of whole rows in turn, loads the next one while it works on this, and keeps its dg
+// in registers until the end.  Each value is read once and written once.  1.3B layer (8192 x 16 x 128
+// bf16) 33.5 us, 168 MB at 5.0 TB/s; 12345 x 32 x 256 from 8 bits 163 us, 815 MB at 5.0 TB/s; fp32 layer
+// 58 us.  Bound by latency at 16 warps per SM: the exponential and the reciprocal keep the special
+// function units 37 % busy, issue slots are 41 to 49 % used.  More warps need fewer registers than the
+// three rows of values take: 8 values per lane at 24 or 32 warps ran 35 and 34 us, and 171 and 163 us.
 
 template <typename T> constexpr int EPI_CHANNELS = 32 / sizeof(T);  // per lane: one 32-byte vector
 constexpr int EPI_THREADS = 256, EPI_BLOCKS = 2;                    // blocks per SM: 128 registers
@@ -216,15 +223,22 @@ cudaError_t epilogue_t(const EpilogueBwdArgs &a, float *parts, cudaStream_t stre
 // (token, head) row, and walks a run of R tokens forwards.  dx_t is complete once dy_{t+K-1} is known, so three unfinished dx and the
 // three previous x stay in registers beside the taps and their gradients; each run walks K - 1 tokens
 // further than it writes.  The taps' gradients of a run leave as one row of partial sums; within it
-// they are sums of sums over 256 tokens, so that a long run's rounding does not grow with its length.  Every lane
-// also takes the gate of its path's width (alpha with q, b with k, w with v) at the same offsets: the
-// gates are pure traffic, the convolutions mostly arithmetic, and so the two overlap.
+// they are sums of sums over 256 tokens, so that a long run's rounding does not grow with its length.
+//
+// The convolutions are bound by arithmetic (about 130 instructions per lane and token for 16 bytes read
+// and 8 written: 93 us of the 1.3B layer without the gates, whose bytes take 49 us), so the gates, pure
+// streams, are blocks of their own: the runs take seven eighths of the SMs' room, and the gates' blocks
+// the rest and what the runs leave.  Together 118 us, 604 MB at 5.1 TB/s; 15003 packed tokens x 32
+// heads, d_v = 256, from 8 bits 525 us, 2474 MB at 4.7 TB/s; the layer in fp32 190 us, 1208 MB at 6.4
+// TB/s.  What was slower: 8 channels per lane (spills, 185 us), the gates in the convolution's lanes
+// (142 us), run length and path varying inside a block, with the norm's lanes known only at run time
+// (138 us), shorter runs in several rounds (154 to 184 us), a fifth block per SM (128 us).
 
 constexpr int CT = 128;           // threads of a block, at most
 constexpr int CONV_BLOCKS = 4;    // blocks of that many threads per SM
 constexpr int GATE_TILES = 32;    // blocks of the gates per SM, at most
 constexpr int SUM_BATCHES = 64;   // load batches after which the taps' gradients move to their second level
-constexpr int CS = 2;             // load batches in a lane's ring (one is used, the other in flight)
+constexpr int CS = 2;             // load batches in a lane's ring (one is used, the other in flight; a third: no gain)
 
 struct PathBwd {  // a convolution path and the gate that goes with it
   const void *x, *d, *gx, *gd;

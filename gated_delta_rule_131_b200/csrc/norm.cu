@@ -10,6 +10,11 @@
 // Both are HBM-bound streams.  A row is held in the registers of `span` threads, NE values each, so it
 // is read once; the statistics are sums over those threads, the variance taken about the mean.  Threads
 // walk rows in turn and load the next one before the sums of this one meet.
+//
+// 8192 x 2048 bf16: forward with a residual 25 us, 134 MB at 5.3 TB/s (fp32 46 us, 5.8 TB/s); backward
+// with dh 33 us, 134 MB at 4.1 TB/s, of which about 5 us are the second launch (fp32 51 us, 5.2 TB/s);
+// from 8 bits 31 us.  Both are bound by latency: two barriers a row forward, one backward, at 50 to 63 %
+// of the issue slots; 16 values per thread halve the sums' share (8: 37 us backward, 33 forward).
 #include <algorithm>
 #include <utility>
 
