@@ -659,3 +659,70 @@ def test_offsets_past_32_bits(g):
     ref = g.block_prologue_bwd(*ts, *conv, *ts, cu_seqlens=torch.tensor([0, 40], dtype=torch.int32, device="cuda"))
     for p, q in zip(outs[:6], ref[:6]):
         assert torch.equal(p[-40:], q)
+
+
+FIRST_CALL = """
+import torch, gated_delta_rule_131_b200 as g
+bf = torch.bfloat16
+r = lambda *s: torch.randn(*s, device="cuda").to(bf)
+x, w = r(40, 512), torch.ones(512, device="cuda")
+mean, rstd = torch.zeros(40, device="cuda"), torch.ones(40, device="cuda")
+o, nw = r(30, 2, 64), torch.ones(64, device="cuda")
+t, conv = [r(1, 20, 2, 64) for _ in range(12)], [torch.randn(128, 4, device="cuda") for _ in range(3)]
+def calls():
+    a = g.act_pack(t[:6])
+    n = g.layer_norm_fwd(x, w, residual=x, checkpoint=True)
+    return [n.y, *g.layer_norm_bwd(x, x, mean, rstd, w), *g.block_epilogue_bwd(o, o, nw, o),
+            *g.block_prologue_bwd(*a, *conv, *t[6:]), *g.act_unpack(a)]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip(out, calls()))
+print("captured first")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    """The pool, the kernels' limits and the kernels themselves are set up inside a stream capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.abspath(os.path.join(os.path.dirname(__file__), ".."))
+    run = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "captured first" in run.stdout, run.stderr[-2000:]
+
+
+def test_what_the_binding_turns_down(g):
+    """Layouts and devices that the library does not take, before anything is launched."""
+    before = g.launch_count()
+    x, w = rand(1, 8, 128, dtype=torch.bfloat16), rand(2, 128)
+    n = rand(3, 8)
+    bad = [lambda: g.layer_norm_fwd(x.t(), rand(4, 8)), lambda: g.layer_norm_fwd(x, w.cpu()),
+           lambda: g.layer_norm_fwd(x, w, stream="not a stream"),
+           lambda: g.layer_norm_bwd(x, x, n, n.cpu(), w), lambda: g.act_pack(x[:, ::2]), lambda: g.act_pack([x] * 9),
+           lambda: g.act_pack(x.flatten()[1:129]),  # not on a 16-byte boundary
+           lambda: g.layer_norm_fwd(rand(5, 2, 8200), rand(6, 8200)),
+           lambda: g.block_epilogue_bwd(*[rand(i, 4, 2, 96) for i in (1, 2)], rand(3, 96), rand(4, 4, 2, 96)),
+           lambda: g.block_prologue_bwd(*[rand(i, 1, 4, 2, 64) for i in range(6)], *[rand(i, 128, 5) for i in range(3)],
+                                        *[rand(i, 1, 4, 2, 64) for i in range(6)])]
+    for call in bad:
+        with pytest.raises((ValueError, g.Gdn2Error, AttributeError)):
+            call()
+    assert g.launch_count() == before
+
+
+def test_the_same_tensor_in_every_place(g):
+    x, w = rand(1, 70, 128, dtype=torch.bfloat16), rand(2, 128)
+    same, apart = g.layer_norm_fwd(x, w, w, residual=x), g.layer_norm_fwd(x, w, w.clone(), residual=x.clone())
+    assert all(torch.equal(p, q) for p, q in zip(same[:4], apart[:4]))
+    b = g.layer_norm_bwd(x, x, same.mean, same.rstd, w, dh=x)
+    for p, q in zip(b, g.layer_norm_bwd(x.clone(), x, same.mean, same.rstd, w, dh=x.clone())):
+        assert torch.equal(p, q)
+    a = g.act_pack([x, x])
+    assert torch.equal(a[0].codes, a[1].codes) and torch.equal(a[0].scales, a[1].scales)
+    t, c = rand(3, 1, 33, 2, 64), rand(4, 128, 4)
+    for p, q in zip(g.block_prologue_bwd(*[t] * 6, c, c, c, *[t] * 6),
+                    g.block_prologue_bwd(*[t.clone() for _ in range(6)], c, c, c, *[t.clone() for _ in range(6)])):
+        assert torch.equal(p, q)
