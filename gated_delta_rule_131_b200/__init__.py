@@ -99,7 +99,7 @@ def lib():
         L.gdn2_layer_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
         L.gdn2_block_epilogue_bwd.argtypes = [vp] * 9 + [cll, ci, ci, ci, vp]
         L.gdn2_block_epilogue_bwd.restype = ci
-        L.gdn2_block_epilogue_bwd_workspace_bytes.argtypes = [cll, ci, ci]
+        L.gdn2_block_epilogue_bwd_workspace_bytes.argtypes = [cll, ci, ci, ci]
         L.gdn2_block_epilogue_bwd_workspace_bytes.restype = ctypes.c_size_t
         L.gdn2_block_prologue_bwd.argtypes = [vp] * 25 + [ci] * 6 + [vp, ci, vp]
         L.gdn2_block_prologue_bwd.restype = ci
@@ -624,9 +624,9 @@ def block_epilogue_bwd(o, gate, norm_weight, dy, stream=None):
     return do, dgate, dnorm_weight
 
 
-def block_epilogue_bwd_workspace_bytes(tokens, H, d_v) -> int:
+def block_epilogue_bwd_workspace_bytes(tokens, H, d_v, dtype=torch.bfloat16) -> int:
     """Device bytes ``block_epilogue_bwd`` takes from the library's pool for this shape."""
-    return int(lib().gdn2_block_epilogue_bwd_workspace_bytes(tokens, H, d_v))
+    return int(lib().gdn2_block_epilogue_bwd_workspace_bytes(tokens, H, d_v, _DTYPES[dtype]))
 
 
 _PRE = ("xq", "xk", "xv", "xa", "xb", "xw")

@@ -186,13 +186,14 @@ cudaError_t launch_recurrent(const RecurrentArgs &a, bool bf16, bool r2, cudaStr
 cudaError_t launch_block_prologue(const BlockPrologueArgs &p, bool bf16, cudaStream_t stream);
 cudaError_t launch_block_epilogue(const BlockEpilogueArgs &p, bool bf16, cudaStream_t stream);
 // The training operators of the block.  The backward passes write rows of partial weight gradients
-// into a workspace of the given bytes (for the current device) and sum them in a second launch.
+// into a workspace of the given bytes (for the current device) and sum them in a second launch; with
+// none (0 bytes, a null workspace) the few blocks of a short call sum them as one cluster.
 cudaError_t launch_act_pack(const ActArgs &a, bool bf16, cudaStream_t stream);
 cudaError_t launch_act_unpack(const ActArgs &a, bool bf16, cudaStream_t stream);
 cudaError_t launch_norm_fwd(const NormFwdArgs &a, bool bf16, cudaStream_t stream);
 size_t norm_bwd_workspace_bytes(long long rows, int width, bool bf16);
 cudaError_t launch_norm_bwd(const NormBwdArgs &a, bool bf16, void *ws, cudaStream_t stream);
-size_t epilogue_bwd_workspace_bytes(long long rows, int dv);
+size_t epilogue_bwd_workspace_bytes(long long rows, int dv, bool bf16);
 cudaError_t launch_epilogue_bwd(const EpilogueBwdArgs &a, bool bf16, void *ws, cudaStream_t stream);
 size_t prologue_bwd_workspace_bytes(long long tokens, int H, int dk, int dv, int K);
 cudaError_t launch_prologue_bwd(const PrologueBwdArgs &a, bool bf16, void *ws, cudaStream_t stream);

@@ -96,6 +96,7 @@ cudaError_t run_chunk_bwd(const gdn2::BwdArgs &a, bool bf16, cudaStream_t stream
 // which needs the relaxed capture mode for this thread.
 template <typename F>
 cudaError_t with_workspace(size_t bytes, cudaStream_t stream, F launch) {
+  if (bytes == 0) return launch(nullptr);
   cudaMemPool_t pool;
   void *ws = nullptr;
   cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
@@ -481,13 +482,14 @@ gdn2_status gdn2_block_epilogue_bwd(const void *o, const void *gate, const uint8
   const cudaStream_t s = (cudaStream_t)stream;
   if (tokens == 0) return finish(cudaMemsetAsync(dnorm_weight, 0, d_v * sizeof(float), s));
   const gdn2::EpilogueBwdArgs a{o, gate, dy, o_scales, gate_scales, norm_weight, d_o, dgate, dnorm_weight, tokens * H, d_v};
-  return finish(with_workspace(gdn2::epilogue_bwd_workspace_bytes(a.rows, d_v), s,
+  return finish(with_workspace(gdn2::epilogue_bwd_workspace_bytes(a.rows, d_v, dtype == GDN2_BF16), s,
                                [&](void *ws) { return gdn2::launch_epilogue_bwd(a, dtype == GDN2_BF16, ws, s); }));
 }
 
-size_t gdn2_block_epilogue_bwd_workspace_bytes(long long tokens, int H, int d_v) {
+size_t gdn2_block_epilogue_bwd_workspace_bytes(long long tokens, int H, int d_v, gdn2_dtype dtype) {
   if (tokens <= 0 || H <= 0 || !supported_dv(d_v) || !fits(tokens, H, d_v, 4)) return 0;
-  return gdn2::epilogue_bwd_workspace_bytes(tokens * H, d_v);
+  if (dtype != GDN2_F32 && dtype != GDN2_BF16) return 0;
+  return gdn2::epilogue_bwd_workspace_bytes(tokens * H, d_v, dtype == GDN2_BF16);
 }
 
 gdn2_status gdn2_block_prologue_bwd(const void *x_q, const void *x_k, const void *x_v, const void *x_alpha,

@@ -359,9 +359,9 @@ GDN2_API gdn2_status gdn2_layer_norm_fwd(const void *x, const void *residual, co
  *   mean, rstd : as the forward returned them     weight : as in the forward
  *   dweight, dbias : [width] fp32 out, written (not added to); dbias may be NULL
  * dx may alias dy or dh.  All sums in fp32 in a fixed order: the results are reproducible on one kind
- * of device.  Takes gdn2_layer_norm_bwd_workspace_bytes() bytes from the library's pool (partial sums)
- * and gives them back on `stream`.  Sizes, alignment and errors as for the forward.  tokens == 0
- * writes zeros to dweight and dbias.
+ * of device.  Takes gdn2_layer_norm_bwd_workspace_bytes() bytes from the library's pool (partial sums;
+ * 0 for a short call) and gives them back on `stream`.  Sizes, alignment and errors as for the forward.
+ * tokens == 0 writes zeros to dweight and dbias.
  */
 GDN2_API gdn2_status gdn2_layer_norm_bwd(const void *dy, const void *h, const uint8_t *h_scales, const float *mean,
                                          const float *rstd, const float *weight, const void *dh, void *dx,
@@ -385,7 +385,7 @@ GDN2_API gdn2_status gdn2_block_epilogue_bwd(const void *o, const void *gate, co
                                              const uint8_t *gate_scales, const float *norm_weight, const void *dy,
                                              void *d_o, void *dgate, float *dnorm_weight, long long tokens, int H,
                                              int d_v, gdn2_dtype dtype, gdn2_stream_t stream);
-GDN2_API size_t gdn2_block_epilogue_bwd_workspace_bytes(long long tokens, int H, int d_v);
+GDN2_API size_t gdn2_block_epilogue_bwd_workspace_bytes(long long tokens, int H, int d_v, gdn2_dtype dtype);
 
 /*
  * gdn2_block_prologue_bwd -- gradients through gdn2_block_prologue, from the gradients that

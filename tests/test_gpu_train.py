@@ -175,8 +175,7 @@ def test_layer_norm_constant_row_and_a_row_with_nan(g):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("width", WIDTHS)
 @pytest.mark.parametrize("ckpt,along", [(False, True), (True, False), (True, True)])
-def test_layer_norm_bwd(g, dtype, width, ckpt, along):
-    tokens = 149
+def test_layer_norm_bwd(g, dtype, width, ckpt, along, tokens=149):
     h = rand(1, tokens, width, dtype=dtype, shift=0.5)
     dy = rand(2, tokens, width, dtype=dtype)
     dh = rand(3, tokens, width, dtype=dtype) if along else None
@@ -195,6 +194,20 @@ def test_layer_norm_bwd(g, dtype, width, ckpt, along):
     again = g.layer_norm_bwd(dy, held, out.mean, out.rstd, w, dh=dh)
     assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), again))  # sums in a fixed order
     assert g.layer_norm_bwd(dy, held, out.mean, out.rstd, w, dh=dh, want_dbias=False)[2] is None
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width,tokens", [(w, t) for w in (1, 37, 1001, 2048, 8192) for t in (1, 7, 8, 9)]
+                         + [(64, 17), (64, 127), (64, 128), (64, 129), (256, 31), (256, 32), (256, 33), (1024, 8)])
+def test_layer_norm_bwd_of_few_rows(g, dtype, width, tokens):
+    """Either side of the sizes that one cluster of blocks does in a single launch."""
+    if width > 1:  # a row of one value has no variance
+        test_layer_norm_bwd(g, dtype, width, tokens % 2 == 0, tokens % 3 != 0, tokens)
+    else:
+        dy, h, one = rand(1, tokens, 1, dtype=dtype), rand(2, tokens, 1, dtype=dtype), torch.ones(tokens, device="cuda")
+        dw, db = g.layer_norm_bwd(dy, h, 0 * one, one, rand(3, 1))[1:]
+        close(dw, (np64(dy) * np64(h)).sum(0), np.abs(np64(dy) * np64(h)).sum(0), C_SUM, "dweight")
+        close(db, np64(dy).sum(0), np.abs(np64(dy)).sum(0), C_SUM, "dbias")
 
 
 def off16(t):
@@ -286,6 +299,15 @@ def test_epilogue_bwd(g, dtype, dv, tokens, H, ckpt):
     close(dg, rg, (np.abs(dy64) * aoh * s).sum((0, 1)), C_SUM, "dnorm_weight")
     again = g.block_epilogue_bwd(oh_, zh, nw, dy)
     assert all(torch.equal(p, q) for p, q in zip((do, dz, dg), again))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dv,rows", [(64, (255, 513, 1024, 1025)), (128, (33, 256, 257, 512, 513)),
+                                     (256, (9, 128, 129, 256, 257))])
+def test_epilogue_bwd_of_few_rows(g, dtype, dv, rows):
+    """Either side of the sizes that one cluster of blocks does in a single launch."""
+    for n in rows:
+        test_epilogue_bwd(g, dtype, dv, n, 1, n % 2 == 0)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -566,7 +588,8 @@ def test_block_training_step_from_checkpoints(g):
 # --------------------------------------------------------------------- streams, graphs, sizes past 2^31
 
 def _calls(g):
-    """Each backward call on inputs of its own, as closures that return their outputs."""
+    """Each backward call on inputs of its own, as closures that return their outputs; the short ones
+    (one launch of one cluster) beside the others."""
     bf = torch.bfloat16
     x, w = rand(1, 300, 1000, dtype=bf), rand(2, 1000)
     n = g.layer_norm_fwd(x, w)
@@ -580,6 +603,8 @@ def _calls(g):
 
     return [norm,
             lambda **k: list(g.layer_norm_bwd(x, n.h, n.mean, n.rstd, w, **k)),
+            lambda **k: list(g.layer_norm_bwd(x[:7], n.h[:7], n.mean[:7], n.rstd[:7], w, **k)),
+            lambda **k: list(g.block_epilogue_bwd(o[:11], z[:11], nw, dy[:11], **k)),
             lambda **k: list(g.block_epilogue_bwd(o, z, nw, dy, **k)),
             lambda **k: list(g.block_prologue_bwd(*pre[:6], *conv, *pre[6:], **k)),
             lambda **k: list(g.block_prologue_bwd(*acts, *conv, *pre[6:], **k)),

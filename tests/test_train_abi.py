@@ -162,21 +162,25 @@ def test_act_refusals(L, name):
 
 
 def test_workspace_bytes(L):
-    """One row of partial weight gradients for each block (148 SMs where there is no GPU)."""
-    assert L.gdn2_layer_norm_bwd_workspace_bytes(1, 100, BF16) == 2 * 100 * 4
-    assert L.gdn2_layer_norm_bwd_workspace_bytes(0, 100, BF16) == 0
-    assert L.gdn2_layer_norm_bwd_workspace_bytes(5, 8193, BF16) == 0
-    assert L.gdn2_layer_norm_bwd_workspace_bytes(5, 64, 7) == 0
-    assert L.gdn2_block_epilogue_bwd_workspace_bytes(1, 1, 64) == 64 * 4
-    assert L.gdn2_block_epilogue_bwd_workspace_bytes(1, 1, 63) == 0
+    """One row of partial weight gradients for each block (148 SMs where there is no GPU); none where the
+    few blocks of a short call are one cluster."""
+    norm, epi = L.gdn2_layer_norm_bwd_workspace_bytes, L.gdn2_block_epilogue_bwd_workspace_bytes
+    assert norm(8192, 2048, BF16) == 148 * 2 * 2048 * 4 == gdn2.layer_norm_bwd_workspace_bytes(8192, 2048)
+    # a cluster is 8 blocks, of one row each or of sums of up to 1024 channels (width 256: four rows)
+    assert norm(8, 2048, BF16) == 0 and norm(9, 2048, BF16) == 9 * 2 * 2048 * 4
+    assert norm(32, 256, BF16) == 0 and norm(33, 256, BF16) == 33 * 2 * 256 * 4
+    assert norm(0, 100, BF16) == norm(5, 8193, BF16) == norm(5, 64, 7) == 0
+    assert epi(8192, 16, 128, BF16) == 296 * 128 * 4 == gdn2.block_epilogue_bwd_workspace_bytes(8192, 16, 128)
+    # 256 threads x 16 channels: 32 rows of 128 a tile, two tiles for each of 8 blocks are the last cluster
+    assert epi(512, 1, 128, BF16) == 0 and epi(513, 1, 128, BF16) == 17 * 128 * 4
+    assert epi(256, 1, 128, gdn2.GDN2_F32) == 0 and epi(257, 1, 128, gdn2.GDN2_F32) == 17 * 128 * 4
+    assert epi(5000, 1, 63, BF16) == epi(5000, 1, 64, 9) == 0
     n = L.gdn2_block_prologue_bwd_workspace_bytes(1, 2, 1, 64, 128, 3, 0, gdn2.GDN2_F32)
     assert n == (64 + 64 + 128) * 3 * 4  # one run
     assert L.gdn2_block_prologue_bwd_workspace_bytes(1, 2, 1, 64, 128, 5, 0, gdn2.GDN2_F32) == 0
     # bounded by the resident lanes however many tokens there are
     big = L.gdn2_block_prologue_bwd_workspace_bytes(64, 65536, 16, 128, 128, 4, 0, BF16)
     assert 0 < big < 64 << 20
-    assert gdn2.layer_norm_bwd_workspace_bytes(1, 100) == 800
-    assert gdn2.block_epilogue_bwd_workspace_bytes(1, 1, 64) == 256
     assert gdn2.block_prologue_bwd_workspace_bytes(1, 2, 1, 64, 128, 3, dtype=torch.float32) == n
 
 
