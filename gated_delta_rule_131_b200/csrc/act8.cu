@@ -244,8 +244,8 @@ cudaError_t act_t(const ActArgs &all, cudaStream_t stream) {
 }
 
 // Column sums, 3 to 5 us behind the kernel that wrote the rows, most of it the launch and one round trip
-// to the L2.  A block sums 32 columns (lane = column): warp w takes the rows w, w + W, ... of its W warps, eight
-// loads in flight and added as a tree, then the first warp adds the warps' sums in order.
+// to the L2.  A block sums 32 columns (lane = column): warp w takes the rows w, w + W, ... of its W
+// warps, eight loads in flight and added as a tree, then the first warp adds the warps' sums in order.
 constexpr int SUM_WARPS = 32;
 __global__ void __launch_bounds__(32 * SUM_WARPS) colsum_kernel(const ColSumArgs a) {
   __shared__ float part[SUM_WARPS][32];

@@ -217,8 +217,8 @@ cudaError_t epilogue_t(const EpilogueBwdArgs &a, float *parts, cudaStream_t stre
 
 template <typename T, typename S>
 cudaError_t epilogue_t(const EpilogueBwdArgs &a, float *parts, cudaStream_t stream) {
-  const bool wide = on32((const char *)a.dy, (const char *)a.dout, (const char *)a.dz, sizeof(S) == 1 ? nullptr : (const char *)a.o,
-                         sizeof(S) == 1 ? nullptr : (const char *)a.z);
+  const bool wide = on32((const char *)a.dy, (const char *)a.dout, (const char *)a.dz,
+                         sizeof(S) == 1 ? nullptr : (const char *)a.o, sizeof(S) == 1 ? nullptr : (const char *)a.z);
   return wide ? epilogue_t<T, S, 32>(a, parts, stream) : epilogue_t<T, S, 16>(a, parts, stream);
 }
 
@@ -231,10 +231,11 @@ cudaError_t epilogue_t(const EpilogueBwdArgs &a, float *parts, cudaStream_t stre
 // Gates: alpha = sigmoid(-x), b and w = sigmoid(x): dx = +- d p (1 - p), p = sigmoid(x).
 //
 // A block holds up to 512 neighbouring channels of one path, 4 per lane, so that d / 4 lanes hold one
-// (token, head) row, and walks a run of R tokens forwards.  dx_t is complete once dy_{t+K-1} is known, so three unfinished dx and the
-// three previous x stay in registers beside the taps and their gradients; each run walks K - 1 tokens
-// further than it writes.  The taps' gradients of a run leave as one row of partial sums; within it
-// they are sums of sums over 256 tokens, so that a long run's rounding does not grow with its length.
+// (token, head) row, and walks a run of R tokens forwards.  dx_t is complete once dy_{t+K-1} is known,
+// so three unfinished dx and the three previous x stay in registers beside the taps and their
+// gradients; each run walks K - 1 tokens further than it writes.  The taps' gradients of a run leave as
+// one row of partial sums; within it they are sums of sums over 256 tokens, so that a long run's
+// rounding does not grow with its length.
 //
 // The convolutions are bound by arithmetic (about 130 instructions per lane and token for 16 bytes read
 // and 8 written: 93 us of the 1.3B layer without the gates, whose bytes take 49 us), so the gates, pure
@@ -593,7 +594,7 @@ ConvBwdPlan conv_bwd_plan(long long tokens, int H, int dk, int dv, int K) {
   int per_run = 0;
   for (int i = 0; i < 3; ++i) per_run += p.blocks[i] = (H * dim[i] / CC + p.threads - 1) / p.threads;
   const long long slots = (long long)sm_count() * CONV_BLOCKS * (CT / p.threads);
-    const long long runs = std::max(1ll, slots * 7 / 8 / per_run), R = ((tokens + runs - 1) / runs + 3) / 4 * 4;
+  const long long runs = std::max(1ll, slots * 7 / 8 / per_run), R = ((tokens + runs - 1) / runs + 3) / 4 * 4;
   p.R = (int)std::min(R, most);
   p.runs = (tokens + p.R - 1) / p.R;
   p.ncols = H * (2 * dk + dv) * K;

@@ -305,8 +305,8 @@ GDN2_API gdn2_status gdn2_block_epilogue(const void *o, const void *gate, const 
  * 2^e, e >= -126, with max |x| <= 127 * 2^e, stored as e + 127; code = x / 2^e rounded to the nearest
  * integer, ties to even.  The value that is held, code * 2^e, is within 2^(e-1) of x (under 1/126 of
  * the group's largest value) and exact in fp32 and bf16.  Finite values above 127 * 2^121 are held as
- * that.  A group holding an infinity or a NaN has
- * scale 255 and zero codes and reads back as NaN.  33/32 bytes per value.
+ * that.  A group holding an infinity or a NaN has scale 255 and zero codes and reads back as NaN.
+ * 33/32 bytes per value.
  *
  * gdn2_layer_norm_fwd writes its rows in this form beside its output; gdn2_layer_norm_bwd,
  * gdn2_block_epilogue_bwd and gdn2_block_prologue_bwd read it in place of the saved activations.
@@ -377,9 +377,9 @@ GDN2_API size_t gdn2_layer_norm_bwd_workspace_bytes(long long tokens, int width,
  *   o, gate  : the forward's inputs in dtype, or, with o_scales and gate_scales (both or neither),
  *              their int8 codes (above; groups of 32 channels within a head)
  *   dy, d_o, dgate : [tokens, H, d_v] (dtype, 16-byte aligned)   dnorm_weight : [d_v] fp32 out, written
- * d_o and dgate may alias dy, o or gate of the same type (each its own buffer).  fp32 arithmetic and sums, in a fixed order.
- * Takes gdn2_block_epilogue_bwd_workspace_bytes() bytes from the library's pool.  tokens == 0 writes
- * zeros to dnorm_weight.  Asynchronous on `stream`; errors as for gdn2_block_epilogue.
+ * d_o and dgate may alias dy, o or gate of the same type (each its own buffer).  fp32 arithmetic and
+ * sums, in a fixed order.  Takes gdn2_block_epilogue_bwd_workspace_bytes() bytes from the library's
+ * pool (0 for a short call).  tokens == 0 writes zeros to dnorm_weight.  Asynchronous on `stream`; errors as for gdn2_block_epilogue.
  */
 GDN2_API gdn2_status gdn2_block_epilogue_bwd(const void *o, const void *gate, const uint8_t *o_scales,
                                              const uint8_t *gate_scales, const float *norm_weight, const void *dy,
@@ -399,9 +399,9 @@ GDN2_API size_t gdn2_block_epilogue_bwd_workspace_bytes(long long tokens, int H,
  *   conv_*     : as in the forward        dq .. dw, dx_q .. dx_w : layouts of x_q .. x_w (dtype)
  *   dconv_q, dconv_k [H * d_k, conv_len], dconv_v [H * d_v, conv_len] : fp32 out, written
  * Layouts (dense, or packed with cu_seqlens), sizes, alignment and errors as for gdn2_block_prologue;
- * H at most GDN2_PROLOGUE_BWD_MAX_HEADS (GDN2_ERR_INVALID_ARG).  In a packed batch T may exceed cu_seqlens[B]: the rows behind the last
- * sequence are not read and their gradients not written.  Outputs must not overlap inputs.  fp32
- * arithmetic; sums in fp32 in a fixed order.  Takes gdn2_block_prologue_bwd_workspace_bytes() bytes
+ * H at most GDN2_PROLOGUE_BWD_MAX_HEADS (GDN2_ERR_INVALID_ARG).  In a packed batch T may exceed
+ * cu_seqlens[B]: the rows behind the last sequence are not read and their gradients not written.
+ * Outputs must not overlap inputs.  fp32 arithmetic; sums in fp32 in a fixed order.  Takes gdn2_block_prologue_bwd_workspace_bytes() bytes
  * from the library's pool.  Without tokens (B == 0 or T == 0) zeros go to dconv_*.
  */
 #define GDN2_PROLOGUE_BWD_MAX_HEADS 65536

@@ -12,6 +12,7 @@ roundings on the longest way from an input to the result:
 What is held in 8 bits, and a residual sum, have to be equal.
 """
 import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -621,6 +622,30 @@ def test_calls_on_two_other_streams_at_once(g):
     for per in outs:
         for i, got in enumerate(per):
             assert all(torch.equal(a, b) for a, b in zip(got, refs[i // 5]))
+
+
+def test_calls_from_two_threads_at_once(g):
+    calls = _calls(g)
+    refs = [c() for c in calls]
+    torch.cuda.synchronize()
+    outs = [[], []]
+
+    def work(out):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                out.append([c() for c in calls])
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(out,)) for out in outs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for out in outs:
+        assert len(out) == 20
+        for turn in out:
+            for got, ref in zip(turn, refs):
+                assert all(torch.equal(a, b) for a, b in zip(got, ref))
 
 
 def test_captured_calls_replay(g):
