@@ -237,14 +237,14 @@ cudaError_t epilogue_t(const EpilogueBwdArgs &a, float *parts, cudaStream_t stre
 // one row of partial sums; within it they are sums of sums over 256 tokens, so that a long run's
 // rounding does not grow with its length.
 //
-// The convolutions are bound by arithmetic (about 130 instructions per lane and token for 16 bytes read
-// and 8 written: 93 us of the 1.3B layer without the gates, whose bytes take 49 us), so the gates, pure
-// streams, are blocks of their own: the runs take seven eighths of the SMs' room, and the gates' blocks
-// the rest and what the runs leave.  Together 118 us, 604 MB at 5.1 TB/s; 15003 packed tokens x 32
-// heads, d_v = 256, from 8 bits 525 us, 2474 MB at 4.7 TB/s; the layer in fp32 190 us, 1208 MB at 6.4
-// TB/s.  What was slower: 8 channels per lane (spills, 185 us), the gates in the convolution's lanes
-// (142 us), run length and path varying inside a block, with the norm's lanes known only at run time
-// (138 us), shorter runs in several rounds (154 to 184 us), a fifth block per SM (128 us).
+// The convolutions are bound by arithmetic (about 125 instructions per lane and token for 16 bytes read
+// and 8 written), so the gates, pure streams, are blocks of their own: the runs take seven eighths of the
+// SMs' room (three quarters: 119 us, all of it: 118), and the gates' blocks the rest and what the runs
+// leave.  1.3B layer 115 us, 604 MB at 5.3 TB/s (the runs alone 100 us, the gates alone 49); 15003
+// packed tokens x 32 heads, d_v = 256, from 8 bits 517 us, 2474 MB at 4.8 TB/s; the layer in fp32 190 us,
+// 1208 MB at 6.4 TB/s.  What was slower: 8 channels per lane (spills, 185 us), the gates in the
+// convolution's lanes (142 us), run length and path varying inside a block, with the norm's lanes known
+// only at run time (138 us), shorter runs in several rounds (154 to 184 us), a fifth block per SM (128 us).
 
 constexpr int CT = 128;           // threads of a block, at most
 constexpr int CONV_BLOCKS = 4;    // blocks of that many threads per SM
@@ -423,62 +423,90 @@ __device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P,
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     int lo = 0;  // first token of the run in the current sequence
-    auto token = [&](int i, const uint8_t *from, float unit, auto checked) {
+    // One token, or two whose sums meet together: nine shuffles instead of twelve, and one's arithmetic
+    // fills the other's waits (1.3B layer 115 us; one at a time 118).
+    auto token = [&](int i, const uint8_t *from, uint32_t units, auto checked, auto count) {
       constexpr bool CHECK = decltype(checked)::value;
-      const unsigned o = (unsigned)i * stride + ch;
-      Pairs<CC> xt, y, g, ds;
-      Lane<S, CC> rx;
+      constexpr int NT = decltype(count)::value;
+      Pairs<CC> xt[NT], y[NT], g[NT], ds[NT];
       Lane<T, CC> rd;
-      rx.v[0] = *reinterpret_cast<const LaneVec<S, CC> *>(from + RB::X + threadIdx.x * RB::XB);
-      rd.v[0] = *reinterpret_cast<const LaneVec<T, CC> *>(from + RB::D + threadIdx.x * RB::DB);
-      rx.get(xt, unit);
-      rd.get(g, 0.f);
 #pragma unroll
-      for (int c = 0; c < CC / 2; ++c) {
-        float2 v = __fmul2_rn(w[0].p[c], xt.p[c]);
-        v = __ffma2_rn(w[1].p[c], x1.p[c], v);
-        v = __ffma2_rn(w[2].p[c], x2.p[c], v);
-        v = __ffma2_rn(w[3].p[c], x3.p[c], v);
-        const float2 sg = sigmoid2(v);
-        y.p[c] = __fmul2_rn(v, sg);
-        ds.p[c] = __ffma2_rn(y.p[c], one_minus2(sg), sg);  // derivative of SiLU
-      }
-      if constexpr (G > 0) {
-        // both sums in one pass: even lanes end with sum y^2, odd ones with sum y d
-        const float ss = dot(y, y), sd = dot(y, g);
-        const bool odd = lane & 1;
-        float s = (odd ? sd : ss) + __shfl_xor_sync(gmask, odd ? ss : sd, 1);
-#pragma unroll
-        for (int m = 2; m < G; m <<= 1) s += __shfl_xor_sync(gmask, s, m);
-        const float other = __shfl_xor_sync(gmask, s, 1);
-        const float nrm = rsqrt_approx((odd ? other : s) + L2_EPS), k3 = -nrm * nrm * nrm * (odd ? s : other);
-#pragma unroll
-        for (int c = 0; c < CC / 2; ++c) g.p[c] = __ffma2_rn(splat(k3), y.p[c], __fmul2_rn(splat(nrm), g.p[c]));
-      }
-#pragma unroll
-      for (int c = 0; c < CC / 2; ++c) g.p[c] = __fmul2_rn(g.p[c], ds.p[c]);  // dy
-      if (!CHECK || i < ntok) {
+      for (int t = 0; t < NT; ++t) {
+        const Pairs<CC> &h1 = t == 1 ? xt[0] : x1, &h2 = t == 1 ? x1 : x2, &h3 = t == 1 ? x2 : x3;
+        Lane<S, CC> rx;
+        rx.v[0] = *reinterpret_cast<const LaneVec<S, CC> *>(from + t * RB::TOKEN + RB::X + threadIdx.x * RB::XB);
+        rd.v[0] = *reinterpret_cast<const LaneVec<T, CC> *>(from + t * RB::TOKEN + RB::D + threadIdx.x * RB::DB);
+        rx.get(xt[t], Q ? act8_unit(units >> 8 * t & 255) : 0.f);
+        rd.get(g[t], 0.f);
 #pragma unroll
         for (int c = 0; c < CC / 2; ++c) {
-          dw[0].p[c] = __ffma2_rn(g.p[c], xt.p[c], dw[0].p[c]);
-          dw[1].p[c] = __ffma2_rn(g.p[c], x1.p[c], dw[1].p[c]);
-          dw[2].p[c] = __ffma2_rn(g.p[c], x2.p[c], dw[2].p[c]);
-          dw[3].p[c] = __ffma2_rn(g.p[c], x3.p[c], dw[3].p[c]);
+          float2 v = __fmul2_rn(w[0].p[c], xt[t].p[c]);
+          v = __ffma2_rn(w[1].p[c], h1.p[c], v);
+          v = __ffma2_rn(w[2].p[c], h2.p[c], v);
+          v = __ffma2_rn(w[3].p[c], h3.p[c], v);
+          const float2 sg = sigmoid2(v);
+          y[t].p[c] = __fmul2_rn(v, sg);
+          ds[t].p[c] = __ffma2_rn(y[t].p[c], one_minus2(sg), sg);  // derivative of SiLU
         }
       }
+      if constexpr (G > 0) {
+        // all sums in one pass: even lanes end with sum y^2, odd ones with sum y d, of the first token
+        // where lane & 2 is 0
+        const bool odd = lane & 1, second = NT == 2 && lane & 2;
+        float part[NT];
 #pragma unroll
-      for (int c = 0; c < CC / 2; ++c) {
-        y.p[c] = __ffma2_rn(w[3].p[c], g.p[c], p3.p[c]);  // dx of the third token before
-        p3.p[c] = __ffma2_rn(w[2].p[c], g.p[c], p2.p[c]);
-        p2.p[c] = __ffma2_rn(w[1].p[c], g.p[c], p1.p[c]);
-        p1.p[c] = __fmul2_rn(w[0].p[c], g.p[c]);
+        for (int t = 0; t < NT; ++t) {
+          const float ss = dot(y[t], y[t]), sd = dot(y[t], g[t]);
+          part[t] = (odd ? sd : ss) + __shfl_xor_sync(gmask, odd ? ss : sd, 1);
+        }
+        float s = part[0];
+        if constexpr (NT == 2) s = (second ? part[1] : part[0]) + __shfl_xor_sync(gmask, second ? part[0] : part[1], 2);
+#pragma unroll
+        for (int m = 2 * NT; m < G; m <<= 1) s += __shfl_xor_sync(gmask, s, m);
+        const float other = __shfl_xor_sync(gmask, s, 1);
+        const float n = rsqrt_approx((odd ? other : s) + L2_EPS), k = -n * n * n * (odd ? s : other);
+        float nrm[2] = {n, n}, k3[2] = {k, k};
+        if constexpr (NT == 2) {
+          const float on = __shfl_xor_sync(gmask, n, 2), ok = __shfl_xor_sync(gmask, k, 2);
+          nrm[0] = second ? on : n;
+          k3[0] = second ? ok : k;
+          nrm[1] = second ? n : on;
+          k3[1] = second ? k : ok;
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int c = 0; c < CC / 2; ++c)
+            g[t].p[c] = __ffma2_rn(splat(k3[t]), y[t].p[c], __fmul2_rn(splat(nrm[t]), g[t].p[c]));
       }
-      x3 = x2;
-      x2 = x1;
-      x1 = xt;
-      if (i - 3 >= lo) {
-        rd.put(y);
-        rd.store(dx + (o - 3 * stride));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const unsigned o = (unsigned)(i + t) * stride + ch;
+#pragma unroll
+        for (int c = 0; c < CC / 2; ++c) g[t].p[c] = __fmul2_rn(g[t].p[c], ds[t].p[c]);  // dy
+        if (!CHECK || i < ntok) {
+#pragma unroll
+          for (int c = 0; c < CC / 2; ++c) {
+            dw[0].p[c] = __ffma2_rn(g[t].p[c], xt[t].p[c], dw[0].p[c]);
+            dw[1].p[c] = __ffma2_rn(g[t].p[c], x1.p[c], dw[1].p[c]);
+            dw[2].p[c] = __ffma2_rn(g[t].p[c], x2.p[c], dw[2].p[c]);
+            dw[3].p[c] = __ffma2_rn(g[t].p[c], x3.p[c], dw[3].p[c]);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < CC / 2; ++c) {
+          y[t].p[c] = __ffma2_rn(w[3].p[c], g[t].p[c], p3.p[c]);  // dx of the third token before
+          p3.p[c] = __ffma2_rn(w[2].p[c], g[t].p[c], p2.p[c]);
+          p2.p[c] = __ffma2_rn(w[1].p[c], g[t].p[c], p1.p[c]);
+          p1.p[c] = __fmul2_rn(w[0].p[c], g[t].p[c]);
+        }
+        x3 = x2;
+        x2 = x1;
+        x1 = xt[t];
+        if (i + t - 3 >= lo) {
+          rd.put(y[t]);
+          rd.store(dx + (o - 3 * stride));
+        }
       }
     };
     // What is unfinished before token i is complete where its sequence ends at i.
@@ -513,7 +541,8 @@ __device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P,
       const uint8_t *slot = ring + (bt % CS) * RB::BATCH;
       if (ib + CU <= ntok && nbr >= ib + CU) {  // a full batch inside one sequence: no checks
 #pragma unroll
-        for (int u = 0; u < CU; ++u) token(ib + u, slot + u * RB::TOKEN, act8_unit(now >> 8 * u & 255), std::false_type());
+        for (int u = 0; u < CU; u += 2)
+          token(ib + u, slot + u * RB::TOKEN, now >> 8 * u, std::false_type(), std::integral_constant<int, 2>());
         i = ib + CU;
       } else {
 #pragma unroll 1
@@ -539,7 +568,7 @@ __device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P,
               nbr = nb <= t ? INT_MAX : (int)min(nb - t0, (long long)INT_MAX);
             }
           }
-          token(i, slot + u * RB::TOKEN, act8_unit(now >> 8 * u & 255), std::true_type());
+          token(i, slot + u * RB::TOKEN, now >> 8 * u, std::true_type(), std::integral_constant<int, 1>());
           ++i;
         }
       }
