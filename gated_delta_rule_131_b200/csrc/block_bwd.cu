@@ -67,15 +67,15 @@ template <typename S, int N, int WB = 16> struct Lane {
 };
 
 // d <- sign d p (1 - p), p = sigmoid(x): p (1 - p) = e / (1 + e)^2 with e = 2^-(|x| log2 e), which neither
-// cancels nor overflows, and 1 + e <= 2 lets one reciprocal serve a pair.
+// cancels nor overflows.  Each channel has a reciprocal of its own: one of the pair's product would carry a
+// channel's NaN to the other (and saved nothing: 1.3B layer 114.9 us, packed from 8 bits 516 for 517).
 template <int N> __device__ __forceinline__ void gate_bwd(const Pairs<N> &x, Pairs<N> &d, float sign) {
 #pragma unroll
   for (int c = 0; c < N / 2; ++c) {
     const float2 e = make_float2(ex2_approx(-1.4426950408889634f * fabsf(x.p[c].x)),
                                  ex2_approx(-1.4426950408889634f * fabsf(x.p[c].y)));
     const float2 den = __fadd2_rn(e, splat(1.f));
-    const float r = rcp_approx(den.x * den.y);
-    const float2 p = __fmul2_rn(splat(r), make_float2(den.y, den.x));
+    const float2 p = make_float2(rcp_approx(den.x), rcp_approx(den.y));
     d.p[c] = __fmul2_rn(__fmul2_rn(d.p[c], e), __fmul2_rn(p, __fmul2_rn(p, splat(sign))));
   }
 }
