@@ -323,8 +323,11 @@ __device__ __forceinline__ void gates_bwd(const ConvBwdArgs &a, int block) {
   }
 }
 
-// One block's run of one path; G: lanes of a row whose norm is taken, 0 for a path without one.
-template <typename T, typename S, int G>
+// One block's run of one path; G: lanes of a row whose norm is taken, 0 for a path without one.  FOUR:
+// there are four taps; where there are fewer, the others' products are left out, not formed with zeros
+// (0 * NaN would carry a NaN to tokens that the taps do not join).  The common four-tap form so pays
+// nothing for them.
+template <typename T, typename S, int G, bool FOUR>
 __device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P, int blk, long long run, uint8_t *ring,
                                          float4 (*far)[CT]) {
   using RB = Ring<T, S>;
@@ -332,6 +335,7 @@ __device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P,
   constexpr bool Q = sizeof(S) == 1;
   const long long t0 = run * a.R;
   const int K = a.K;
+  const bool has1 = FOUR || K > 1, has2 = FOUR || K > 2;  // the last tap is there where FOUR
   const unsigned stride = (unsigned)a.H * P.dim;  // elements between tokens; a run's offsets fit 32 bits
   const unsigned ch = (blk * blockDim.x + threadIdx.x) * CC;
   if (ch >= stride) return;  // whole groups leave together
@@ -441,9 +445,9 @@ __device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P,
 #pragma unroll
         for (int c = 0; c < CC / 2; ++c) {
           float2 v = __fmul2_rn(w[0].p[c], xt[t].p[c]);
-          v = __ffma2_rn(w[1].p[c], h1.p[c], v);
-          v = __ffma2_rn(w[2].p[c], h2.p[c], v);
-          v = __ffma2_rn(w[3].p[c], h3.p[c], v);
+          if (has1) v = __ffma2_rn(w[1].p[c], h1.p[c], v);
+          if (has2) v = __ffma2_rn(w[2].p[c], h2.p[c], v);
+          if (FOUR) v = __ffma2_rn(w[3].p[c], h3.p[c], v);
           const float2 sg = sigmoid2(v);
           y[t].p[c] = __fmul2_rn(v, sg);
           ds[t].p[c] = __ffma2_rn(y[t].p[c], one_minus2(sg), sg);  // derivative of SiLU
@@ -495,9 +499,9 @@ __device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P,
         }
 #pragma unroll
         for (int c = 0; c < CC / 2; ++c) {
-          y[t].p[c] = __ffma2_rn(w[3].p[c], g[t].p[c], p3.p[c]);  // dx of the third token before
-          p3.p[c] = __ffma2_rn(w[2].p[c], g[t].p[c], p2.p[c]);
-          p2.p[c] = __ffma2_rn(w[1].p[c], g[t].p[c], p1.p[c]);
+          y[t].p[c] = FOUR ? __ffma2_rn(w[3].p[c], g[t].p[c], p3.p[c]) : p3.p[c];  // dx of the third token before
+          p3.p[c] = has2 ? __ffma2_rn(w[2].p[c], g[t].p[c], p2.p[c]) : p2.p[c];
+          p2.p[c] = has1 ? __ffma2_rn(w[1].p[c], g[t].p[c], p1.p[c]) : p1.p[c];
           p1.p[c] = __fmul2_rn(w[0].p[c], g[t].p[c]);
         }
         x3 = x2;
@@ -589,7 +593,7 @@ __device__ __forceinline__ void conv_bwd(const ConvBwdArgs &a, const PathBwd &P,
   }
 }
 
-template <typename T, typename S>
+template <typename T, typename S, bool FOUR>
 __global__ void __launch_bounds__(CT, CONV_BLOCKS) prologue_bwd_kernel(const ConvBwdArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float4 far[4][CT];
@@ -603,9 +607,9 @@ __global__ void __launch_bounds__(CT, CONV_BLOCKS) prologue_bwd_kernel(const Con
   const long long run = cb / per_run;
   int blk = (int)(cb % per_run), path = 0;
   while (path < 2 && blk >= a.path[path].blocks) blk -= a.path[path++].blocks;
-  if (path == 2) conv_bwd<T, S, 0>(a, a.path[2], blk, run, ring, far);
-  else if (a.path[0].dim == 64) conv_bwd<T, S, 64 / CC>(a, a.path[path], blk, run, ring, far);
-  else conv_bwd<T, S, 128 / CC>(a, a.path[path], blk, run, ring, far);
+  if (path == 2) conv_bwd<T, S, 0, FOUR>(a, a.path[2], blk, run, ring, far);
+  else if (a.path[0].dim == 64) conv_bwd<T, S, 64 / CC, FOUR>(a, a.path[path], blk, run, ring, far);
+  else conv_bwd<T, S, 128 / CC, FOUR>(a, a.path[path], blk, run, ring, far);
 }
 
 // How the work is cut; the same for the workspace's size and the launch.  Runs are as many as let all
@@ -630,7 +634,7 @@ ConvBwdPlan conv_bwd_plan(long long tokens, int H, int dk, int dv, int K) {
   return p;
 }
 
-template <typename T, typename S>
+template <typename T, typename S, bool FOUR>
 cudaError_t prologue_t(const PrologueBwdArgs &p, float *parts, cudaStream_t stream) {
   const ConvBwdPlan pl = conv_bwd_plan(p.tokens, p.H, p.dk, p.dv, p.K);
   const int dim[3] = {p.dk, p.dk, p.dv};
@@ -660,13 +664,18 @@ cudaError_t prologue_t(const PrologueBwdArgs &p, float *parts, cudaStream_t stre
   a.gate_blocks = (int)std::min<long long>(tiles, (long long)sm_count() * GATE_TILES);
   constexpr int smem = CS * Ring<T, S>::BATCH;
   static std::atomic<uint64_t> allowed;
-  cudaError_t err = allow_smem((const void *)prologue_bwd_kernel<T, S>, smem, allowed);
+  cudaError_t err = allow_smem((const void *)prologue_bwd_kernel<T, S, FOUR>, smem, allowed);
   if (err != cudaSuccess) return err;
   note_launch();
   const long long blocks = pl.runs * (pl.blocks[0] + pl.blocks[1] + pl.blocks[2]);
-  prologue_bwd_kernel<T, S><<<(unsigned)(blocks + a.gate_blocks), pl.threads, smem, stream>>>(a);
+  prologue_bwd_kernel<T, S, FOUR><<<(unsigned)(blocks + a.gate_blocks), pl.threads, smem, stream>>>(a);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   return launch_colsum(sum, stream);
+}
+
+template <typename T, typename S>
+cudaError_t prologue_t(const PrologueBwdArgs &p, float *parts, cudaStream_t stream) {
+  return p.K == 4 ? prologue_t<T, S, true>(p, parts, stream) : prologue_t<T, S, false>(p, parts, stream);
 }
 
 }  // namespace

@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_train import C_ROW, HALF, TYPES, U, g, np64, rand  # noqa: F401
+from oracle import block_train as bt
+from test_gpu_train import C_ROW, C_SUM, HALF, TYPES, U, conv_major, g, hold, np64, rand  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,30 @@ def test_gates_keep_a_nan_in_its_channel(g, dtype):
         ref = (-1.0 if i == 3 else 1.0) * np64(d[i]) * p * (1.0 - p)
         # an infinity shuts its gate: p (1 - p) = 0
         close_where_finite(outs[i], ref, np.where(np.isnan(ref), 0.0, np.abs(ref)), C_ROW, ("xa", "xb", "xw")[i - 3])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("K", [1, 2, 3, 4])
+@pytest.mark.parametrize("ckpt", [False, True])
+def test_a_nan_reaches_as_far_as_the_taps(g, dtype, K, ckpt):
+    """A NaN in an input moves the gradients of the K - 1 tokens before and after that its taps join, in
+    its head alone; with fewer than four taps there is no fourth one that it could pass through."""
+    B, T, H, dims = 2, 60, 3, (64, 64, 64, 64, 64, 64)
+    x = [rand(i, B, T, H, d, dtype=dtype) for i, d in enumerate(dims)]
+    d = [rand(10 + i, B, T, H, n, dtype=dtype) for i, n in enumerate(dims)]
+    conv = [rand(20 + i, H * n, K) for i, n in enumerate(dims[:3])]
+    for i in range(3):
+        x[i][0, 20, 1, 5] = x[i][0, 31, 1, 40] = float("nan")  # first and last token of a run
+        x[i][0, T - 1, 0, 7] = float("nan")                    # the next sequence starts afresh
+        d[i][1, 9, 2, 63] = d[i][1, T - 1, 1, 0] = float("nan")
+    held = [hold(g, t, ckpt) for t in x]
+    outs = g.block_prologue_bwd(*[h for h, _ in held], *conv, *d)
+    flat = lambda v: v.reshape(B * T, H, -1)  # noqa: E731
+    x64, d64, c64 = [flat(v) for _, v in held], [flat(np64(t)) for t in d], [np64(c) for c in conv]
+    cu = [0, T, 2 * T]
+    refs = bt.block_prologue_bwd(*x64, *c64, *d64, cu_seqlens=cu)
+    for i in range(3):
+        # what is finite does not depend on the NaN, so the majorants need not either
+        mx, mW = conv_major(np.nan_to_num(x64[i], nan=0.0), c64[i], np.nan_to_num(d64[i], nan=0.0), i < 2, cu)
+        close_where_finite(flat(outs[i]), refs[i], mx, C_ROW, "xqxkxv"[2 * i:2 * i + 2])
+        close_where_finite(outs[6 + i], refs[6 + i], mW, C_SUM, "conv")
