@@ -114,7 +114,9 @@ __device__ __forceinline__ void pack(const float2 (&f)[CE / 2], uint4 (&r)[2]) {
 // that two batches are in flight while one is used; each lane reads back only its own copies, so
 // the block never synchronises.  Every row is read once (plus three halo rows per run) and written
 // once.  grid = (blocks of the widest path, 3 paths); the host picks R so that the grid is one wave.
-template <typename T>
+// FOUR: there are four taps; where there are fewer, the others' products are left out, not formed with
+// zeros (0 * NaN would carry a NaN to tokens that the taps do not join).
+template <typename T, bool FOUR>
 __global__ void __launch_bounds__(256, 2) conv_silu_kernel(const ConvArgs a) {
   constexpr int NV = CE * (int)sizeof(T) / 16;  // 16-byte vectors per lane and token
   constexpr int CU = 8 / NV;                    // tokens per load batch
@@ -207,9 +209,9 @@ __global__ void __launch_bounds__(256, 2) conv_silu_kernel(const ConvArgs a) {
 #pragma unroll
     for (int k = 0; k < CE / 2; ++k) {
       float2 c = __fmul2_rn(w0[k], xt[k]);
-      c = __ffma2_rn(w1[k], x1[k], c);
-      c = __ffma2_rn(w2[k], x2[k], c);
-      c = __ffma2_rn(w3[k], x3[k], c);
+      if (FOUR || a.K > 1) c = __ffma2_rn(w1[k], x1[k], c);
+      if (FOUR || a.K > 2) c = __ffma2_rn(w2[k], x2[k], c);
+      if (FOUR) c = __ffma2_rn(w3[k], x3[k], c);
       y[k] = silu2(c);
       ss = __ffma2_rn(y[k], y[k], ss);
       x3[k] = x2[k];
@@ -337,9 +339,9 @@ __global__ void __launch_bounds__(256) rms_gate_kernel(const T *o, const T *z, c
 
 constexpr int CONV_SMEM = CS * 8 * 16 * 256;  // the ring: CS batches of 8 16-byte vectors per thread
 
-// Resident 256-thread blocks of conv_silu_kernel<T> on the current device (per SM times SMs); sets
+// Resident 256-thread blocks of conv_silu_kernel<T, FOUR> on the current device (per SM times SMs); sets
 // the kernel's shared-memory limit on first use.
-template <typename T>
+template <typename T, bool FOUR>
 cudaError_t conv_slots(int &slots) {
   static int cache[64] = {};
   int dev = 0;
@@ -350,9 +352,9 @@ cudaError_t conv_slots(int &slots) {
     return cudaSuccess;
   }
   int per_sm = 0, sms = 0;
-  err = cudaFuncSetAttribute(conv_silu_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, CONV_SMEM);
+  err = cudaFuncSetAttribute(conv_silu_kernel<T, FOUR>, cudaFuncAttributeMaxDynamicSharedMemorySize, CONV_SMEM);
   if (err == cudaSuccess)
-    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, conv_silu_kernel<T>, 256, CONV_SMEM);
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, conv_silu_kernel<T, FOUR>, 256, CONV_SMEM);
   if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (err != cudaSuccess) return err;
   slots = std::max(1, per_sm) * std::max(1, sms);
@@ -360,12 +362,12 @@ cudaError_t conv_slots(int &slots) {
   return cudaSuccess;
 }
 
-template <typename T>
+template <typename T, bool FOUR>
 cudaError_t prologue_t(const BlockPrologueArgs &p, cudaStream_t stream) {
   if (p.tokens <= 0) return cudaSuccess;
   constexpr int CU = 8 * 16 / (CE * (int)sizeof(T));  // tokens a lane loads at once (as in the kernel)
   int slots = 0;
-  cudaError_t err = conv_slots<T>(slots);
+  cudaError_t err = conv_slots<T, FOUR>(slots);
   if (err != cudaSuccess) return err;
   ConvArgs a{};
   a.path[0] = ConvPath{p.xq, p.Wq, p.q, p.dk, 1};
@@ -384,7 +386,7 @@ cudaError_t prologue_t(const BlockPrologueArgs &p, cudaStream_t stream) {
   const long long runs = (p.tokens + a.R - 1) / a.R;
   const long long blocks = (runs * p.H * (std::max(p.dk, p.dv) / CE) + 255) / 256;
   note_launch();
-  conv_silu_kernel<T><<<dim3((unsigned)blocks, 3), 256, CONV_SMEM, stream>>>(a);
+  conv_silu_kernel<T, FOUR><<<dim3((unsigned)blocks, 3), 256, CONV_SMEM, stream>>>(a);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   const size_t nk = (size_t)p.tokens * p.H * p.dk, nv = (size_t)p.tokens * p.H * p.dv;
@@ -414,7 +416,8 @@ cudaError_t epilogue_t(const BlockEpilogueArgs &p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_block_prologue(const BlockPrologueArgs &p, bool bf16, cudaStream_t stream) {
-  return bf16 ? prologue_t<__nv_bfloat16>(p, stream) : prologue_t<float>(p, stream);
+  if (p.K == 4) return bf16 ? prologue_t<__nv_bfloat16, true>(p, stream) : prologue_t<float, true>(p, stream);
+  return bf16 ? prologue_t<__nv_bfloat16, false>(p, stream) : prologue_t<float, false>(p, stream);
 }
 
 cudaError_t launch_block_epilogue(const BlockEpilogueArgs &p, bool bf16, cudaStream_t stream) {

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from oracle import block_train as bt
 from test_gpu_train import C_ROW, C_SUM, HALF, TYPES, U, conv_major, g, hold, np64, rand  # noqa: F401
 
@@ -68,3 +69,24 @@ def test_a_nan_reaches_as_far_as_the_taps(g, dtype, K, ckpt):
         mx, mW = conv_major(np.nan_to_num(x64[i], nan=0.0), c64[i], np.nan_to_num(d64[i], nan=0.0), i < 2, cu)
         close_where_finite(flat(outs[i]), refs[i], mx, C_ROW, "xqxkxv"[2 * i:2 * i + 2])
         close_where_finite(outs[6 + i], refs[6 + i], mW, C_SUM, "conv")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("K", [1, 2, 3, 4])
+def test_a_nan_reaches_as_far_as_the_taps_forward(g, dtype, K):
+    """The forward of the same: tokens more than K - 1 behind a NaN are those of the formula.  Tolerances
+    are the forward's own (``test_gpu_block.py``)."""
+    B, T, H, d = 2, 60, 3, 64
+    x = [rand(i, B, T, H, d, dtype=dtype) for i in range(6)]
+    conv = [rand(20 + i, H * d, K) for i in range(3)]
+    for t in x[:3]:
+        t[0, 20, 1, 5] = t[0, 31, 1, 40] = t[0, T - 1, 0, 7] = float("nan")
+    outs = g.block_prologue(*x, *conv)
+    for got, ref in zip(outs, oracle.block_prologue(*[np64(t) for t in x], *[np64(c) for c in conv])):
+        got, nan = np64(got), np.isnan(ref)
+        assert np.array_equal(np.isnan(got), nan)
+        err = np.abs(got - ref)[~nan]
+        if dtype is torch.float32:
+            assert err.max() <= 1e-4 * np.abs(ref[~nan]).max()
+        else:
+            assert (err <= 1e-2 + 2e-2 * np.abs(ref[~nan])).all()
