@@ -372,6 +372,7 @@ def decode_step(q, k, v, alpha, b, w, S, o=None, stream=None):
 ACT_GROUP = 32          # channels that share a scale in an Act8
 ACT_MAX_TENSORS = 8     # GDN2_ACT_MAX_TENSORS in include/gdn2.h
 NORM_MAX_WIDTH = 8192   # GDN2_NORM_MAX_WIDTH in include/gdn2.h
+_INT_MAX = 2 ** 31 - 1  # the C ABI's sizes are ints; ctypes would cut larger ones to their low 32 bits
 
 
 class Act8(NamedTuple):
@@ -489,8 +490,8 @@ def act_pack(xs, stream=None):
     for x in xs:
         if x.dtype is not dtype or dtype not in _DTYPES:
             raise ValueError("gdn2: act_pack: the tensors must share dtype float32 or bfloat16")
-        if x.dim() < 1 or x.shape[-1] < 1:
-            raise ValueError("gdn2: act_pack: a tensor needs a last dimension of at least 1")
+        if x.dim() < 1 or not 1 <= x.shape[-1] <= _INT_MAX:
+            raise ValueError("gdn2: act_pack: a tensor needs a last dimension of 1 to 2^31 - 1")
     s = _handle(xs) if stream is None else None
     if s is None:
         return _elsewhere(stream, xs, lambda: act_pack(xs[0] if one else xs))
@@ -508,8 +509,8 @@ def act_unpack(acts, dtype=torch.bfloat16, stream=None):
     if dtype not in _DTYPES:
         raise ValueError("gdn2: act_unpack: dtype must be float32 or bfloat16")
     for a in acts:
-        if a.codes.dim() < 1 or a.codes.shape[-1] < 1:
-            raise ValueError("gdn2: act_unpack: a tensor needs a last dimension of at least 1")
+        if a.codes.dim() < 1 or not 1 <= a.codes.shape[-1] <= _INT_MAX:
+            raise ValueError("gdn2: act_unpack: a tensor needs a last dimension of 1 to 2^31 - 1")
         _check_act8("act_unpack", "act", a, a.codes.shape)
     codes, scales = [a.codes for a in acts], [a.scales for a in acts]
     s = _handle(codes + scales) if stream is None else None
@@ -533,6 +534,8 @@ def layer_norm_fwd(x, weight, bias=None, residual=None, eps=1e-5, checkpoint=Fal
     if not shape or shape[-1] < 1:
         raise ValueError("gdn2: layer_norm_fwd: x needs a last dimension of at least 1")
     D = shape[-1]
+    if D > NORM_MAX_WIDTH:
+        raise Gdn2Error(GDN2_ERR_UNSUPPORTED, "gdn2_layer_norm_fwd")
     _expect(what, "residual", residual, dtype, shape)
     _expect(what, "weight", weight, torch.float32, (D,))
     _expect(what, "bias", bias, torch.float32, (D,))
@@ -570,6 +573,8 @@ def layer_norm_bwd(dy, h, mean, rstd, weight, dh=None, want_dbias=True, stream=N
     if not shape or shape[-1] < 1:
         raise ValueError("gdn2: layer_norm_bwd: dy needs a last dimension of at least 1")
     D = shape[-1]
+    if D > NORM_MAX_WIDTH:
+        raise Gdn2Error(GDN2_ERR_UNSUPPORTED, "gdn2_layer_norm_bwd")
     _expect(what, "dh", dh, dtype, shape)
     _expect(what, "mean", mean, torch.float32, shape[:-1])
     _expect(what, "rstd", rstd, torch.float32, shape[:-1])
@@ -590,7 +595,10 @@ def layer_norm_bwd(dy, h, mean, rstd, weight, dh=None, want_dbias=True, stream=N
 
 
 def layer_norm_bwd_workspace_bytes(tokens, width, dtype=torch.bfloat16) -> int:
-    """Device bytes ``layer_norm_bwd`` takes from the library's pool for this shape."""
+    """Device bytes ``layer_norm_bwd`` takes from the library's pool for this shape (0: none, or a shape
+    that it does not take)."""
+    if abs(width) > _INT_MAX:
+        return 0
     return int(lib().gdn2_layer_norm_bwd_workspace_bytes(tokens, width, _DTYPES[dtype]))
 
 
@@ -608,6 +616,8 @@ def block_epilogue_bwd(o, gate, norm_weight, dy, stream=None):
     if isinstance(o, Act8) != isinstance(gate, Act8):
         raise ValueError("gdn2: block_epilogue_bwd: o and gate are both tensors or both Act8")
     H, dv = shape[-2], shape[-1]
+    if H > _INT_MAX or dv > _INT_MAX:
+        raise Gdn2Error(GDN2_ERR_UNSUPPORTED, "gdn2_block_epilogue_bwd")
     _expect(what, "norm_weight", norm_weight, torch.float32, (dv,))
     oc, osc = _saved(what, "o", o, dy)
     gc, gsc = _saved(what, "gate", gate, dy)
@@ -625,7 +635,10 @@ def block_epilogue_bwd(o, gate, norm_weight, dy, stream=None):
 
 
 def block_epilogue_bwd_workspace_bytes(tokens, H, d_v, dtype=torch.bfloat16) -> int:
-    """Device bytes ``block_epilogue_bwd`` takes from the library's pool for this shape."""
+    """Device bytes ``block_epilogue_bwd`` takes from the library's pool for this shape (0: none, or a
+    shape that it does not take)."""
+    if max(abs(H), abs(d_v)) > _INT_MAX:
+        return 0
     return int(lib().gdn2_block_epilogue_bwd_workspace_bytes(tokens, H, d_v, _DTYPES[dtype]))
 
 
@@ -660,6 +673,8 @@ def block_prologue_bwd(xq, xk, xv, xa, xb, xw, conv_q, conv_k, conv_v, dq, dk, d
         B = cu_seqlens.numel() - 1
         T, H, d_k = shape
     d_v, K = dv.shape[-1], conv_q.shape[1]
+    if max(B, T, H, d_k, d_v, K) > _INT_MAX:
+        raise Gdn2Error(GDN2_ERR_UNSUPPORTED, "gdn2_block_prologue_bwd")
     vshape = torch.Size((*shape[:-1], d_v))
     shapes = (shape, shape, vshape, shape, shape, vshape)
     for i in range(6):
@@ -689,6 +704,9 @@ def block_prologue_bwd(xq, xk, xv, xa, xb, xw, conv_q, conv_k, conv_v, dq, dk, d
 
 
 def block_prologue_bwd_workspace_bytes(B, T, H, d_k, d_v, conv_len, packed=False, dtype=torch.bfloat16) -> int:
-    """Device bytes ``block_prologue_bwd`` takes from the library's pool for this shape."""
+    """Device bytes ``block_prologue_bwd`` takes from the library's pool for this shape (0: a shape that it
+    does not take)."""
+    if max(abs(n) for n in (B, T, H, d_k, d_v, conv_len)) > _INT_MAX:
+        return 0
     return int(lib().gdn2_block_prologue_bwd_workspace_bytes(B, T, H, d_k, d_v, conv_len, int(bool(packed)),
                                                              _DTYPES[dtype]))
