@@ -82,28 +82,36 @@ __global__ void __launch_bounds__(256) act_unpack_flat_kernel(const ActArgs a) {
   }
 }
 
+// How rows of `width` channels are cut into segments of `span` of them, a warp's at a time.  A row may have
+// 2^31 - 1 channels: columns, which run past its end by up to a segment, are unsigned.
+struct Segments {
+  unsigned width, per_row, groups;
+  __host__ __device__ Segments(int w, unsigned span)
+      : width((unsigned)w), per_row((width + span - 1) / span), groups((width + ACT_GROUP - 1) / ACT_GROUP) {}
+};
+
 // Rows that end inside a group but start on 16-byte boundaries: a warp takes 32 * VEC * NU channels of
 // one row at a time.
 template <typename T, int VEC, bool PACK>
 __global__ void __launch_bounds__(256) act_rows_kernel(const ActArgs a) {
-  constexpr int SPAN = 32 * VEC * NU;
+  constexpr unsigned SPAN = 32 * VEC * NU;
   const ActTensor &t = a.t[blockIdx.y];
-  const int per_row = (t.width + SPAN - 1) / SPAN, lane = threadIdx.x & 31;
-  const int groups = (t.width + ACT_GROUP - 1) / ACT_GROUP;
-  const long long tasks = t.rows * per_row, step = (long long)gridDim.x * 8;
+  const Segments g(t.width, SPAN);
+  const unsigned lane = threadIdx.x & 31;
+  const long long tasks = t.rows * g.per_row, step = (long long)gridDim.x * 8;
   for (long long k = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); k < tasks; k += step) {
-    const long long row = k / per_row;
-    const int c0 = (int)(k - row * per_row) * SPAN + lane * VEC;
-    T *x = static_cast<T *>(t.x) + (size_t)row * t.width;
-    int8_t *codes = t.codes + (size_t)row * t.width;
-    uint8_t *scales = t.scales + (size_t)row * groups;
+    const long long row = k / g.per_row;
+    const unsigned c0 = (unsigned)(k - row * g.per_row) * SPAN + lane * VEC;
+    T *x = static_cast<T *>(t.x) + (size_t)row * g.width;
+    int8_t *codes = t.codes + (size_t)row * g.width;
+    uint8_t *scales = t.scales + (size_t)row * g.groups;
     LaneVec<T, VEC> r[NU];
     LaneVec<int8_t, VEC> q[NU];
     uint32_t s[NU];
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const int c = c0 + u * 32 * VEC;  // VEC divides the width: a vector is inside the row or outside
-      if (c < t.width) {
+      const unsigned c = c0 + u * 32 * VEC;  // VEC divides the width: a vector is inside the row or outside
+      if (c < g.width) {
         if constexpr (PACK) {
           r[u].load(x + c);
         } else {
@@ -114,17 +122,17 @@ __global__ void __launch_bounds__(256) act_rows_kernel(const ActArgs a) {
     }
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const int c = c0 + u * 32 * VEC;
+      const unsigned c = c0 + u * 32 * VEC;
       Pairs<VEC> f;
       if constexpr (PACK) {
         widen<0, VEC>(r[u], f);
         uint32_t sc;
-        const LaneVec<int8_t, VEC> v = act8_encode<0>(r[u], f, c < t.width, sc);
-        if (c < t.width) {
+        const LaneVec<int8_t, VEC> v = act8_encode<0>(r[u], f, c < g.width, sc);
+        if (c < g.width) {
           v.store(codes + c);
           if (c % ACT_GROUP == 0) scales[c / ACT_GROUP] = (uint8_t)sc;
         }
-      } else if (c < t.width) {
+      } else if (c < g.width) {
         widen<0, VEC>(q[u], act8_unit(s[u]), f);
         LaneVec<T, VEC> v;
         narrow<0, VEC>(f, v);
@@ -138,28 +146,28 @@ __global__ void __launch_bounds__(256) act_rows_kernel(const ActArgs a) {
 // (read one by one, through the L1), so that two shuffles settle a group's scale.  The codes leave as
 // aligned 4-byte words, each put together from two neighbours; only a segment's ragged ends leave as
 // bytes.  (One channel per lane takes five shuffles per channel: 16384 x 1001 bf16, two tensors, 134 us
-// with the reading back; this form 89 us.)
+// with the reading back; this form 89 us, and 76 with unsigned columns.)
 template <typename T>
 __global__ void __launch_bounds__(256) act_pack_any_kernel(const ActArgs a) {
   constexpr int V = 8, SPAN = 32 * V;
   const ActTensor &t = a.t[blockIdx.y];
-  const int per_row = (t.width + SPAN - 1) / SPAN, lane = threadIdx.x & 31;
-  const int groups = (t.width + ACT_GROUP - 1) / ACT_GROUP;
-  const long long tasks = t.rows * per_row, step = (long long)gridDim.x * 8;
+  const Segments g(t.width, SPAN);
+  const int lane = threadIdx.x & 31;
+  const long long tasks = t.rows * g.per_row, step = (long long)gridDim.x * 8;
   for (long long k = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); k < tasks; k += step) {
-    const long long row = k / per_row;
-    const int first = (int)(k - row * per_row) * SPAN, c = first + lane * V;
-    const T *x = static_cast<const T *>(t.x) + (size_t)row * t.width + c;
+    const long long row = k / g.per_row;
+    const unsigned first = (unsigned)(k - row * g.per_row) * SPAN, c = first + lane * V;
+    const T *x = static_cast<const T *>(t.x) + (size_t)row * g.width + c;
     LaneVec<T, V> r;
 #pragma unroll
-    for (int i = 0; i < V; ++i) r.e[i] = c + i < t.width ? x[i] : T(0.f);
+    for (int i = 0; i < V; ++i) r.e[i] = c + i < g.width ? x[i] : T(0.f);
     Pairs<V> f;
     widen<0, V>(r, f);
     uint32_t sc;
     const LaneVec<int8_t, V> q = act8_encode<0>(r, f, true, sc);
-    if (c < t.width && c % ACT_GROUP == 0) t.scales[(size_t)row * groups + c / ACT_GROUP] = (uint8_t)sc;
-    int8_t *out = t.codes + (size_t)row * t.width + first;
-    const int n = min(SPAN, t.width - first), s = (int)(reinterpret_cast<uintptr_t>(out) & 3);
+    if (c < g.width && c % ACT_GROUP == 0) t.scales[(size_t)row * g.groups + c / ACT_GROUP] = (uint8_t)sc;
+    int8_t *out = t.codes + (size_t)row * g.width + first;
+    const int n = (int)min((unsigned)SPAN, g.width - first), s = (int)(reinterpret_cast<uintptr_t>(out) & 3);
     const uint32_t w0 = reinterpret_cast<const uint32_t *>(&q)[0], w1 = reinterpret_cast<const uint32_t *>(&q)[1];
     const uint32_t before = __shfl_up_sync(0xffffffffu, w1, 1);
     auto put = [&](int at, uint32_t word) {  // the word of bytes at .. at + 3 of the segment
@@ -179,31 +187,31 @@ __global__ void __launch_bounds__(256) act_pack_any_kernel(const ActArgs a) {
 
 template <typename T>
 __global__ void __launch_bounds__(256) act_unpack_any_kernel(const ActArgs a) {
-  constexpr int SPAN = 32 * 2 * NU;
+  constexpr unsigned SPAN = 32 * 2 * NU;
   const ActTensor &t = a.t[blockIdx.y];
-  const int per_row = (t.width + SPAN - 1) / SPAN, lane = threadIdx.x & 31;
-  const int groups = (t.width + ACT_GROUP - 1) / ACT_GROUP;
-  const long long tasks = t.rows * per_row, step = (long long)gridDim.x * 8;
+  const Segments g(t.width, SPAN);
+  const unsigned lane = threadIdx.x & 31;
+  const long long tasks = t.rows * g.per_row, step = (long long)gridDim.x * 8;
   for (long long k = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); k < tasks; k += step) {
-    const long long row = k / per_row;
-    const int c0 = (int)(k - row * per_row) * SPAN + lane;
-    const int8_t *codes = t.codes + (size_t)row * t.width;
-    const uint8_t *scales = t.scales + (size_t)row * groups;
-    T *x = static_cast<T *>(t.x) + (size_t)row * t.width;
+    const long long row = k / g.per_row;
+    const unsigned c0 = (unsigned)(k - row * g.per_row) * SPAN + lane;
+    const int8_t *codes = t.codes + (size_t)row * g.width;
+    const uint8_t *scales = t.scales + (size_t)row * g.groups;
+    T *x = static_cast<T *>(t.x) + (size_t)row * g.width;
     int8_t q[2 * NU];
     uint8_t s[2 * NU];
 #pragma unroll
     for (int u = 0; u < 2 * NU; ++u) {
-      const int c = c0 + 32 * u;
-      if (c < t.width) {
+      const unsigned c = c0 + 32 * u;
+      if (c < g.width) {
         q[u] = codes[c];
         s[u] = scales[c / ACT_GROUP];
       }
     }
 #pragma unroll
     for (int u = 0; u < 2 * NU; ++u) {
-      const int c = c0 + 32 * u;
-      if (c < t.width) x[c] = from_f32<T>((float)q[u] * act8_unit(s[u]));
+      const unsigned c = c0 + 32 * u;
+      if (c < g.width) x[c] = from_f32<T>((float)q[u] * act8_unit(s[u]));
     }
   }
 }
