@@ -430,7 +430,9 @@ def _elsewhere(stream, tensors, call):
 
 
 def _expect(what, name, t, dtype, shape):
-    if t is None or (t.dtype is dtype and t.shape == shape):
+    if t is None:
+        raise ValueError(f"gdn2: {what}: {name} is missing")
+    if t.dtype is dtype and t.shape == shape:
         return
     raise ValueError(f"gdn2: {what}: {name} must be {dtype} of shape {tuple(shape)}, not {t.dtype} of {tuple(t.shape)}")
 
@@ -536,9 +538,11 @@ def layer_norm_fwd(x, weight, bias=None, residual=None, eps=1e-5, checkpoint=Fal
     D = shape[-1]
     if D > NORM_MAX_WIDTH:
         raise Gdn2Error(GDN2_ERR_UNSUPPORTED, "gdn2_layer_norm_fwd")
-    _expect(what, "residual", residual, dtype, shape)
+    if residual is not None:
+        _expect(what, "residual", residual, dtype, shape)
     _expect(what, "weight", weight, torch.float32, (D,))
-    _expect(what, "bias", bias, torch.float32, (D,))
+    if bias is not None:
+        _expect(what, "bias", bias, torch.float32, (D,))
     tensors = (x, weight, bias, residual)
     s = _handle(tensors) if stream is None else None
     if s is None:
@@ -575,7 +579,8 @@ def layer_norm_bwd(dy, h, mean, rstd, weight, dh=None, want_dbias=True, stream=N
     D = shape[-1]
     if D > NORM_MAX_WIDTH:
         raise Gdn2Error(GDN2_ERR_UNSUPPORTED, "gdn2_layer_norm_bwd")
-    _expect(what, "dh", dh, dtype, shape)
+    if dh is not None:
+        _expect(what, "dh", dh, dtype, shape)
     _expect(what, "mean", mean, torch.float32, shape[:-1])
     _expect(what, "rstd", rstd, torch.float32, shape[:-1])
     _expect(what, "weight", weight, torch.float32, (D,))
@@ -662,6 +667,8 @@ def block_prologue_bwd(xq, xk, xv, xa, xb, xw, conv_q, conv_k, conv_v, dq, dk, d
     for x in xs:
         if isinstance(x, Act8) != packed8:
             raise ValueError("gdn2: block_prologue_bwd: the saved inputs are all tensors or all Act8")
+    if dv is None or conv_q is None:
+        raise ValueError("gdn2: block_prologue_bwd: dv and conv_q are needed")
     if len(shape) != (4 if cu_seqlens is None else 3) or not dv.shape or conv_q.dim() != 2:
         raise ValueError("gdn2: block_prologue_bwd: gradients are [B, T, H, d], or [T, H, d] with cu_seqlens; "
                          "convolution weights [H * d, K]")
@@ -678,11 +685,11 @@ def block_prologue_bwd(xq, xk, xv, xa, xb, xw, conv_q, conv_k, conv_v, dq, dk, d
     vshape = torch.Size((*shape[:-1], d_v))
     shapes = (shape, shape, vshape, shape, shape, vshape)
     for i in range(6):
-        if grads[i].dtype is not dtype or grads[i].shape != shapes[i]:
+        if grads[i] is None or grads[i].dtype is not dtype or grads[i].shape != shapes[i]:
             _expect(what, ("dq", "dk", "dv", "dalpha", "db", "dw")[i], grads[i], dtype, shapes[i])
         if packed8:
             _check_act8(what, _PRE[i], xs[i], shapes[i])
-        elif xs[i].dtype is not dtype or xs[i].shape != shapes[i]:
+        elif xs[i] is None or xs[i].dtype is not dtype or xs[i].shape != shapes[i]:
             _expect(what, _PRE[i], xs[i], dtype, shapes[i])
     for i, d in enumerate((d_k, d_k, d_v)):
         _expect(what, ("conv_q", "conv_k", "conv_v")[i], convs[i], torch.float32, (H * d, K))

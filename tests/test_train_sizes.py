@@ -58,3 +58,19 @@ def test_workspace_queries_do_not_cut_sizes():
     assert query(*sizes) > 0
     for i in range(6):
         assert query(*sizes[:i], sizes[i] + 2 ** 32, *sizes[i + 1:]) == 0, i
+
+
+def test_a_missing_tensor_is_named():
+    """What a forward without statistics leaves out, for one: a ValueError, as for every other argument."""
+    h, w, n = meta(4, 64), f32(64), f32(4)
+    x, c, z = [meta(1, 8, 2, 64) for _ in range(6)], [f32(128, 4) for _ in range(3)], meta(4, 2, 64)
+    without = lambda args, i: [None if k == i else a for k, a in enumerate(args)]  # noqa: E731
+    calls = [lambda: gdn2.layer_norm_fwd(h, None)]
+    calls += [lambda i=i: gdn2.layer_norm_bwd(h, *without([h, n, n, w], i)) for i in range(4)]
+    calls += [lambda i=i: gdn2.block_epilogue_bwd(*without([z, z, w], i), z) for i in range(3)]
+    calls += [lambda i=i: gdn2.block_prologue_bwd(*without([*x, *c], i), *x) for i in range(9)]
+    calls += [lambda i=i: gdn2.block_prologue_bwd(*x, *c, *without(x, i)) for i in range(1, 6)]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError) as e:
+            call()
+        assert "CUDA" not in str(e.value), i  # turned down for what is missing, not for where the others are
