@@ -90,3 +90,50 @@ def test_a_nan_reaches_as_far_as_the_taps_forward(g, dtype, K):
             assert err.max() <= 1e-4 * np.abs(ref[~nan]).max()
         else:
             assert (err <= 1e-2 + 2e-2 * np.abs(ref[~nan])).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dv", [64, 256])
+@pytest.mark.parametrize("tokens", [40, 5000])
+def test_epilogue_bwd_keeps_a_nan_in_its_row(g, dtype, dv, tokens):
+    """Rows lie side by side in a warp; a NaN in o, gate or dy reaches what its row's sums join, its channel
+    of the weight's gradient, and nothing else."""
+    H = 3
+    o, z, dy = (rand(i, tokens, H, dv, dtype=dtype) for i in (1, 2, 3))
+    nw = rand(4, dv, scale=0.2, shift=1.0)
+    z[5, 1, 9] = dy[7, 0, 30] = float("nan")
+    outs = g.block_epilogue_bwd(o, z, nw, dy)
+    with_o = o.clone()
+    with_o[11, 2, dv - 1] = float("nan")  # the whole row, and so the whole weight's gradient
+    outs_o = g.block_epilogue_bwd(with_o, z, nw, dy)
+    for o_, got in ((o, outs), (with_o, outs_o)):
+        o64, z64, dy64, nw64 = (np64(t) for t in (o_, z, dy, nw))
+        refs = bt.block_epilogue_bwd(o64, z64, nw64, dy64)
+        o64, z64, dy64 = (np.nan_to_num(t, nan=0.0) for t in (o64, z64, dy64))
+        r = 1 / np.sqrt((o64 ** 2).mean(-1, keepdims=True) + bt.RMS_EPS)
+        sg = 1 / (1 + np.exp(-z64))
+        aoh, s = np.abs(o64) * r, np.abs(z64) * sg
+        ae = np.abs(dy64 * nw64) * s
+        close_where_finite(got[0], refs[0], r * (ae + aoh * (ae * aoh).mean(-1, keepdims=True)), C_ROW, "do")
+        close_where_finite(got[1], refs[1], np.abs(dy64 * nw64) * aoh * (sg + s), C_ROW, "dgate")
+        close_where_finite(got[2], refs[2], (np.abs(dy64) * aoh * s).sum((0, 1)), C_SUM, "dnorm_weight")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width", [64, 100, 513, 2048, 8191])
+@pytest.mark.parametrize("tokens", [8, 700])
+def test_layer_norm_bwd_keeps_a_nan_in_its_row(g, dtype, width, tokens):
+    """A NaN in dy reaches its row's dx and its channel of the weight's and the bias's gradients."""
+    h, dy, dh = (rand(i, tokens, width, dtype=dtype) for i in (1, 2, 3))
+    w = rand(4, width, scale=0.3, shift=1.0)
+    out = g.layer_norm_fwd(h, w)
+    dy[3, 17] = dy[6, width - 1] = float("nan")
+    got = g.layer_norm_bwd(dy, h, out.mean, out.rstd, w, dh=dh)
+    h64, dy64, dh64, w64, mean, rstd = (np64(t) for t in (h, dy, dh, w, out.mean, out.rstd))
+    refs = bt.layer_norm_bwd(dy64, h64, mean, rstd, w64, dh64)
+    dy64 = np.nan_to_num(dy64, nan=0.0)
+    axh, ae = np.abs(h64 - mean[:, None]) * rstd[:, None], np.abs(dy64 * w64)
+    major = rstd[:, None] * (ae + ae.mean(-1, keepdims=True) + axh * (ae * axh).mean(-1, keepdims=True)) + np.abs(dh64)
+    close_where_finite(got[0], refs[0], major, C_ROW, "dx")
+    close_where_finite(got[1], refs[1], (np.abs(dy64) * axh).sum(0), C_SUM, "dweight")
+    close_where_finite(got[2], refs[2], np.abs(dy64).sum(0), C_SUM, "dbias")
