@@ -1,10 +1,11 @@
 // Activation checkpoints in 8 bits (format: act8.cuh): packing, unpacking, and the column sums that
 // finish the weight gradients of the training operators.
 //
-// Packing and unpacking are HBM-bound streams: each value is read once and written once.  Six tensors
-// of the 1.3B layer (100.7 M bf16 values) packed and read back: 97 us, 610 MB at 6.3 TB/s, 0.96 of a
-// copy.  What a value costs is conversion: the group's largest is found on the bf16 pairs as integers,
-// two to an instruction, and the rounding, the products and the widening run in fp32 pairs.
+// Packing and unpacking are HBM-bound streams: each value is read once and written once.  Six tensors of
+// the 1.3B layer (100.7 M bf16 values) packed and read back: 98 us in short runs, 100 us in long ones, 610
+// MB at 6.1 TB/s, 0.93 of a copy.  What a value costs is conversion: the group's largest is found on the
+// bf16 pairs as integers, two to an instruction, and the rounding, the products and the widening run in
+// fp32 pairs.
 #include <algorithm>
 #include <atomic>
 

@@ -4,9 +4,11 @@
 // channels (the last group of a row may be shorter).  The scale is the least power of two 2^e with
 // max |x| <= 127 * 2^e over the group, stored as the fp32 exponent field of 2^e (e + 127, at least 1);
 // the code is x / 2^e rounded to the nearest integer, ties to even.  A power of two makes the
-// scaling exact, so the only error is that one rounding (at most 2^(e-1), under 1/126 of the group's
-// largest value), there is no division, and a code times its scale is exact in fp32 and in bf16.
-// Finite values above 127 * 2^121, which would round up to infinity, are held as that.  A group that
+// scaling exact, so the only error is that one rounding, there is no division, and a code times its scale
+// is exact in fp32 and in bf16.  Finite values above 127 * 2^121, which would round up to infinity, are
+// held as that.  The error is at most 2^(e-1), or 2^121 for a value above 127 * 2^121; either is under 1/127
+// of the group's largest value, as long as that is above 127 * 2^-127.  In a group below it e stays at -126:
+// the error is at most 2^-127, which may be all of a value.  A group that
 // holds an infinity or a NaN has the scale byte 255 and zero codes, and reads back as NaN.
 #pragma once
 

@@ -2,6 +2,9 @@
 // SiLU gate) and of the short convolutions, SiLU, L2 norm and gates in front of it.  The forward is
 // defined in block.cu; here its inputs are read again (in their type, or held in 8 bits) and what the
 // gradients need of the forward is formed anew, in fp32.
+//
+// Figures in this file are of short runs (15 calls back to back) at high clocks, unless they are said to be
+// of long ones (half a second and more, at the clocks that the power limit leaves).
 #include <algorithm>
 #include <climits>
 #include <type_traits>
@@ -68,7 +71,8 @@ template <typename S, int N, int WB = 16> struct Lane {
 
 // d <- sign d p (1 - p), p = sigmoid(x): p (1 - p) = e / (1 + e)^2 with e = 2^-(|x| log2 e), which neither
 // cancels nor overflows.  Each channel has a reciprocal of its own: one of the pair's product would carry a
-// channel's NaN to the other (and saved nothing: 1.3B layer 114.9 us, packed from 8 bits 516 for 517).
+// channel's NaN to the other (and saved nothing: the prologue's 1.3B layer 114.9 us either way, packed from
+// 8 bits 516 us for 517).
 template <int N> __device__ __forceinline__ void gate_bwd(const Pairs<N> &x, Pairs<N> &d, float sign) {
 #pragma unroll
   for (int c = 0; c < N / 2; ++c) {
@@ -101,13 +105,14 @@ __device__ __forceinline__ void cp_async(void *smem, const void *gmem) {
 // do = r (e - oh mean(e oh)), dz = dy g oh sigmoid(z) (1 + z (1 - sigmoid(z))), dg = sum over rows of
 // dy oh s.
 //
-// A row of d_v values is held by G lanes, one 32-byte vector of dy each (16 bf16 or 8 fp32 values); a
-// block takes tiles of whole rows in turn, loads the next one while it works on this, and keeps its dg
-// in registers until the end.  Each value is read once and written once.  1.3B layer (8192 x 16 x 128
-// bf16) 33.5 us, 168 MB at 5.0 TB/s; 12345 x 32 x 256 from 8 bits 163 us, 815 MB at 5.0 TB/s; fp32 layer
-// 58 us.  Bound by latency at 16 warps per SM: the exponential and the reciprocal keep the special
-// function units 37 % busy, issue slots are 41 to 49 % used.  More warps need fewer registers than the
-// three rows of values take: 8 values per lane at 24 or 32 warps ran 35 and 34 us, and 171 and 163 us.
+// A row of d_v values is held by G lanes, one 32-byte vector of dy each (16 bf16 or 8 fp32 values); a block
+// takes tiles of whole rows in turn, loads the next one while it works on this, and keeps its dg in
+// registers until the end.  Each value is read once and written once.  1.3B layer (8192 x 16 x 128 bf16) 34
+// us, 168 MB at 4.9 TB/s; 12345 x 32 x 256 from 8 bits 162 us, 815 MB at 5.0 TB/s (168 us and 4.8 TB/s in
+// long runs); fp32 layer 58 us.  Bound by latency at 16 warps per SM: the exponential and the reciprocal
+// keep the special function units 37 % busy, issue slots are 41 to 49 % used.  More warps need fewer
+// registers than the three rows of values take: 8 values per lane at 24 or 32 warps ran 35 and 34 us, and
+// 171 and 163 us.
 
 template <typename T> constexpr int EPI_CHANNELS = 32 / sizeof(T);  // per lane: one 32-byte vector
 constexpr int EPI_THREADS = 256, EPI_BLOCKS = 2;                    // blocks per SM: 128 registers
@@ -240,9 +245,11 @@ cudaError_t epilogue_t(const EpilogueBwdArgs &a, float *parts, cudaStream_t stre
 // The convolutions are bound by arithmetic (about 125 instructions per lane and token for 16 bytes read
 // and 8 written), so the gates, pure streams, are blocks of their own: the runs take seven eighths of the
 // SMs' room (three quarters: 119 us, all of it: 118), and the gates' blocks the rest and what the runs
-// leave.  1.3B layer 115 us, 604 MB at 5.3 TB/s (the runs alone 100 us, the gates alone 49); 15003
-// packed tokens x 32 heads, d_v = 256, from 8 bits 517 us, 2474 MB at 4.8 TB/s; the layer in fp32 190 us,
-// 1208 MB at 6.4 TB/s.  What was slower: 8 channels per lane (spills, 185 us), the gates in the
+// leave.  1.3B layer 115 us, 604 MB at 5.2 TB/s (the runs alone 100 us, the gates alone 49), in long runs
+// 125 us and 4.8 TB/s; 15003 packed tokens x 32 heads, d_v = 256, from 8 bits 517 us, 2474 MB at 4.8 TB/s,
+// in long runs 566 us and 4.4 TB/s; the layer in fp32 190 us, 1208 MB at 6.4 TB/s.  ptxas reports small
+// spills of the four-tap forms (4 to 40 bytes stored by a thread; none in bf16 from 8 bits) and none of those
+// with fewer taps.  What was slower: 8 channels per lane (spills, 185 us), the gates in the
 // convolution's lanes (142 us), run length and path varying inside a block, with the norm's lanes known
 // only at run time (138 us), shorter runs in several rounds (154 to 184 us), a fifth block per SM (128 us).
 
@@ -257,7 +264,7 @@ struct PathBwd {  // a convolution path and the gate that goes with it
   void *dx, *gdx;
   const uint8_t *scales, *gscales;
   const float *W;
-  int dim, l2, col;  // col: the path's first column in a row of partial sums
+  int dim, col;  // col: the path's first column in a row of partial sums
   float sign;        // of the gate's derivative
   int blocks;        // of one run's channels
 };
@@ -613,8 +620,11 @@ __global__ void __launch_bounds__(CT, CONV_BLOCKS) prologue_bwd_kernel(const Con
 }
 
 // How the work is cut; the same for the workspace's size and the launch.  Runs are as many as let all
-// blocks be resident at once (a second round of a few blocks would double the time), each of at least
-// four tokens and at most what keeps a run's offsets in 32 bits.
+// blocks of CT threads be resident at once (a second round of a few blocks would double the time), each of
+// at least four tokens and at most what keeps a run's offsets in 32 bits.  Blocks of fewer threads (heads of
+// under 512 channels in all) are counted by their threads, but each takes the shared memory of CT: of one
+// head's 16 blocks an SM holds 9 at once in bf16 and 5 in fp32, and such calls run in two to four rounds
+// (15003 tokens x 64 in bf16: 29 us, bytes for 5).
 struct ConvBwdPlan {
   int threads, blocks[3], R, ncols;
   long long runs;
@@ -644,7 +654,7 @@ cudaError_t prologue_t(const PrologueBwdArgs &p, float *parts, cudaStream_t stre
   for (int i = 0; i < 3; ++i) {
     const int g = 3 + i;  // alpha with q, b with k, w with v
     a.path[i] = PathBwd{p.x[i], p.d[i], p.x[g], p.d[g], p.dx[i], p.dx[g], p.scales[i], p.scales[g], p.W[i],
-                        dim[i], i < 2, col, i == 0 ? -1.f : 1.f, pl.blocks[i]};
+                        dim[i], col, i == 0 ? -1.f : 1.f, pl.blocks[i]};
     col += p.H * dim[i] * p.K;
     sum.out[i] = p.dW[i];
     sum.end[i] = col;

@@ -9,12 +9,23 @@
 //
 // Both are HBM-bound streams.  A row is held in the registers of `span` threads, NE values each, so it
 // is read once; the statistics are sums over those threads, the variance taken about the mean.  Threads
-// walk rows in turn and load the next one before the sums of this one meet.
+// walk rows in turn and load the next one before the sums of this one meet, or, where the registers do not
+// hold two, ask for its lines in the L2 (see EARLY).  A column's sums over rows are fp32 sums in one register over the
+// rows of a group (rows / (148 * groups) of them, at most), then over a block's groups, then over the blocks.
 //
 // 8192 x 2048 bf16: forward with a residual 25 us, 134 MB at 5.3 TB/s (fp32 46 us, 5.8 TB/s); backward
 // with dh 33 us, 134 MB at 4.1 TB/s, of which about 5 us are the second launch (fp32 51 us, 5.2 TB/s);
 // from 8 bits 31 us.  Both are bound by latency: two barriers a row forward, one backward, at 50 to 63 %
 // of the issue slots; 16 values per thread halve the sums' share (8: 37 us backward, 33 forward).
+// The backward of that layer was slower with a ring of three rows filled by asynchronous copies in
+// 1024-thread blocks (39 us), two rows at a time (50 us), dh loaded a row ahead (35 us), and its second
+// launch took twice as long with fp64 sums of the columns.
+//
+// Widths that are no multiple of 16 bytes move value by value, far from the bytes they need: backward with dh
+// 8192 x 2047 57 us in bf16, 68 from 8 bits, 60 in fp32, 72 from 8 bits; 4096 x 8191 239, 309, 194 and 247
+// us, where 8192 wide takes 57, 55, 100 and 90.  ptxas reports spills of the backward's forms for them (140 to
+// 350 bytes stored by a thread with 16 values, 36 to 52 with 8 from 8 bits) and of the fp32 form of 16
+// values in 16-byte vectors (44 and 60 bytes).
 #include <algorithm>
 #include <utility>
 

@@ -301,12 +301,13 @@ GDN2_API gdn2_status gdn2_block_epilogue(const void *o, const void *gate, const 
  *
  * They have no counterpart in the pages.  A tensor of `rows` rows of `width` channels is held as
  *   codes  [rows, width] int8 and scales [rows, ceil(width / 32)] uint8:
- * for every 32 channels of a row (the last group of a row may be shorter) the least power of two
- * 2^e, e >= -126, with max |x| <= 127 * 2^e, stored as e + 127; code = x / 2^e rounded to the nearest
- * integer, ties to even.  The value that is held, code * 2^e, is within 2^(e-1) of x (under 1/126 of
- * the group's largest value) and exact in fp32 and bf16.  Finite values above 127 * 2^121 are held as
- * that.  A group holding an infinity or a NaN has scale 255 and zero codes and reads back as NaN.
- * 33/32 bytes per value.
+ * for every 32 channels of a row (the last group of a row may be shorter) the least power of two 2^e, e
+ * >= -126, with max |x| <= 127 * 2^e, stored as e + 127; code = x / 2^e rounded to the nearest integer,
+ * ties to even.  The value that is held, code * 2^e, is exact in fp32 and bf16.  Finite values above
+ * 127 * 2^121 are held as that.  Others are held within 2^(e-1), those within 2^121: under 1/127 of the
+ * group's largest value, unless that is 127 * 2^-127 or less (e = -126), where the error is at most
+ * 2^-127 and may be all of a value.  width: 1 to 2^31 - 1.  A group holding an infinity or a NaN has
+ * scale 255 and zero codes and reads back as NaN.  33/32 bytes per value.
  *
  * gdn2_layer_norm_fwd writes its rows in this form beside its output; gdn2_layer_norm_bwd,
  * gdn2_block_epilogue_bwd and gdn2_block_prologue_bwd read it in place of the saved activations.
@@ -330,8 +331,9 @@ GDN2_API gdn2_status gdn2_act_unpack(const int8_t *const *codes, const uint8_t *
  * gdn2_layer_norm_fwd -- layer norm of the residual stream, in front of the block's projections.
  *
  * The pages name a Transformer-style stack around the block ("NVIDIA AIがGated DeltaNet-2を発表",
- * ai.warp-studio.com, "アーキテクチャとパフォーマンスベンチマーク") and print no norm for it; this is the
- * usual one.  For every token, over its `width` channels:
+ * ai.warp-studio.com, "アーキテクチャとパフォーマンスベンチマーク") and print no norm for it: that it is a layer norm is
+ * this library's own choice (there is no form without the mean).  For every token, over its `width`
+ * channels:
  *   h = x + residual (rounded to dtype; h = x without a residual),
  *   mean = sum h / width, rstd = 1 / sqrt(sum (h - mean)^2 / width + eps),
  *   y = (h - mean) * rstd * weight + bias.
